@@ -1,0 +1,193 @@
+/*
+ * spmv_kv.h -- paged key-value caches on one AMD Instinct MI355X, part of
+ * libspmv.so: block tables and slot maps built on the GPU from request
+ * lengths, new keys and values written to their slots, and the attention of
+ * one new token per request over the cached ones.
+ *
+ * A serving step is a sparse product in disguise: the requests are rows of
+ * very unequal length, the pages they hold are the rows' entries, the block
+ * table is their column index array and the cached keys and values are what
+ * it gathers. The attention shares the rows' tokens out in equal parts, as
+ * the merge-path schedule of spmv.h shares rows + nonzeros.
+ *
+ * Conventions are those of spmv.h: device pointers owned by the caller,
+ * 0-based int32 indices, a status from every function and spmv_last_error()
+ * for its detail, everything enqueued on `stream`, no allocation and no
+ * synchronisation (so every call can be captured in a HIP graph), results
+ * bitwise reproducible (no float atomics; the order in which workgroups end
+ * never changes a sum).
+ *
+ * Words used below. A cache holds n_pages pages of page_size tokens; slot s
+ * is token s % page_size of page s / page_size. A block table is an int32
+ * array of n_requests rows, table_stride entries apart, table_width of them
+ * usable: table[r][j] is the page of request r's tokens j * page_size ...
+ * A pool of free pages is an int32 array of n_free page numbers of which the
+ * first `cursor` are in use and the rest are free.
+ */
+#ifndef SPMV_KV_H_
+#define SPMV_KV_H_
+
+#include "spmv.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element types of caches, queries and new tokens. */
+typedef enum spmv_kv_dtype {
+  SPMV_KV_F32 = 0,
+  SPMV_KV_F16 = 1,
+  SPMV_KV_BF16 = 2,
+  SPMV_KV_F8E4M3 = 3           /* 8-bit float, 4 exponent and 3 mantissa bits,
+                                  no infinities, largest 448; caches only */
+} spmv_kv_dtype_t;
+
+/* One layer's cache. Element (page, token, head, d) of the keys is
+ * k[page * k_page_stride + token * k_token_stride + head * k_head_stride + d]
+ * and of the values the same with v's strides, all in elements, so a layout
+ * with the tokens or the heads of a page outermost is a choice of strides.
+ * k and v and every stride are multiples of 16 bytes (whatever the loads of
+ * a row need), head_dim * element size too; head_dim at most 256. Bytes past
+ * 2^32 are addressed. Borrowed: nothing is copied or kept. */
+typedef struct spmv_kv_cache {
+  void* k;
+  void* v;
+  const float* k_scale;        /* device float[n_heads], F8E4M3 caches only */
+  const float* v_scale;        /* (NULL = 1): a stored byte stands for its
+                                  value times the head's scale */
+  int64_t n_pages;             /* >= 1, n_pages * page_size < 2^31 */
+  int64_t k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+  int32_t page_size;           /* tokens per page, >= 1, any number */
+  int32_t n_heads;             /* key-value heads, >= 1 */
+  int32_t head_dim;
+  int32_t dtype;               /* spmv_kv_dtype_t */
+} spmv_kv_cache_t;
+
+/* What spmv_kv_grow and spmv_kv_shrink write to status[0]; status[1] is the
+ * detail. Read it (or not) when the stream has passed. */
+#define SPMV_KV_OK 0           /* done; detail 0 */
+#define SPMV_KV_NO_PAGES 1     /* detail: pages that are missing (grow), or
+                                  released beyond those in use (shrink) */
+#define SPMV_KV_BAD_ROW 2      /* detail: the first row with a negative count,
+                                  more tokens than its table row holds, or
+                                  (shrink) more kept than there were */
+#define SPMV_KV_NO_ROOM 3      /* detail: new tokens in all, more than
+                                  n_tokens (at most 2^31 - 1 is told) */
+
+/* Requests get longer: pages for the tokens of one step, and where each goes.
+ *
+ *   held[r] = ceil(lengths[r] / page_size)
+ *   need[r] = ceil((lengths[r] + n_new[r]) / page_size) - held[r]
+ *   table[r][held[r] + j] = free_pages[cursor[0] + need[0] + .. + need[r-1] + j]
+ *   token_ptr[r] = n_new[0] + .. + n_new[r-1]      (n_requests + 1 of them)
+ *   lengths_out[r] = lengths[r] + n_new[r]
+ *   cursor_out[0] = cursor[0] + need[0] + .. + need[n_requests - 1]
+ *   for the i-th new token of row r, t = token_ptr[r] + i:
+ *     positions[t] = lengths[r] + i, slots[t] = its slot by the table
+ *   slots[t] = positions[t] = -1 for the rest of the n_tokens entries.
+ *
+ * All or nothing: where status[0] is not SPMV_KV_OK no page is handed out,
+ * the table stays, lengths_out = lengths, cursor_out = cursor and every slot
+ * and position is -1 (token_ptr is written; bad rows count 0 new tokens). A
+ * cursor outside [0, n_free] counts as the nearer end; a page number in the
+ * pool or the table whose slot is not a number of [0, 2^31) gives slot -1.
+ *
+ * lengths, n_new  int32[n_requests]; free_pages int32[n_free]; cursor and
+ * cursor_out int32[1]; status int32[2]. slots and positions int32[n_tokens];
+ * positions may be NULL. No output may overlap another array (the table
+ * counts as both: entries below held[r] are read, those above are written;
+ * lengths_out and cursor_out are arrays of their own, so that a step can be
+ * run again). SPMV_ERR_INVALID_ARG for NULL or overlapping arrays or a
+ * negative size; SPMV_ERR_UNSUPPORTED when table_width * page_size, n_free,
+ * n_requests or n_tokens passes 2^31 - 1. One launch. */
+SPMV_API spmv_status_t spmv_kv_grow(int64_t n_requests, const int32_t* lengths,
+                                    const int32_t* n_new, int32_t page_size,
+                                    const int32_t* free_pages, int64_t n_free,
+                                    const int32_t* cursor, int32_t* table, int64_t table_stride,
+                                    int64_t table_width, int32_t* lengths_out,
+                                    int32_t* cursor_out, int32_t* token_ptr, int32_t* slots,
+                                    int32_t* positions, int64_t n_tokens, int32_t* status,
+                                    hipStream_t stream);
+
+/* Requests get shorter or end (keep 0): their last pages go back to the pool.
+ *
+ *   gone[r] = ceil(lengths[r] / page_size) - ceil(keep[r] / page_size)
+ *   free_pages[cursor[0] - total + gone[0] + .. + gone[r-1] + j]
+ *       = table[r][ceil(keep[r] / page_size) + j], total the sum of gone
+ *   lengths_out[r] = keep[r], cursor_out[0] = cursor[0] - total
+ *
+ * The table is only read: its entries past a row's length mean nothing. All
+ * or nothing, with the arguments and errors of spmv_kv_grow; one launch. */
+SPMV_API spmv_status_t spmv_kv_shrink(int64_t n_requests, const int32_t* lengths,
+                                      const int32_t* keep, int32_t page_size,
+                                      int32_t* free_pages, int64_t n_free,
+                                      const int32_t* cursor, const int32_t* table,
+                                      int64_t table_stride, int64_t table_width,
+                                      int32_t* lengths_out, int32_t* cursor_out,
+                                      int32_t* status, hipStream_t stream);
+
+/* New keys and values to their slots: k[t][h][:] goes to slot slots[t] of the
+ * cache's keys, v[t][h][:] to its values, t < n_tokens. Slots outside
+ * [0, n_pages * page_size) are skipped; the values of a slot named twice are
+ * those of one of its tokens, element by element.
+ *
+ * k, v   device arrays of `dtype` (the cache's, or F32, F16 or BF16 into an
+ *        F8E4M3 cache); element (t, h, d) at t * token_stride +
+ *        h * head_stride + d; any alignment of whole elements.
+ * An F8E4M3 cache stores x / scale[h] (IEEE division in 32 bits) rounded to
+ * nearest even; beyond +-448, infinities included, +-448; NaN stays NaN.
+ * SPMV_ERR_INVALID_ARG for a bad cache, type, NULL array or overlap of k or
+ * v with the cache. One launch. */
+SPMV_API spmv_status_t spmv_kv_append(const spmv_kv_cache_t* cache, int64_t n_tokens,
+                                      const void* k, int64_t k_token_stride,
+                                      int64_t k_head_stride, const void* v,
+                                      int64_t v_token_stride, int64_t v_head_stride,
+                                      int32_t dtype, const int32_t* slots, hipStream_t stream);
+
+/* Attention of one new token per request over its cached tokens. Request r
+ * (the row) has lengths[r] tokens, the newest among them; token t is visible
+ * when t >= lengths[r] - window or t < sinks (window 0: every token; the
+ * first `sinks` tokens stay visible as the window moves on). Query head h
+ * reads key-value head h / (n_q_heads / n_heads).
+ *
+ *   s[t] = scale * sum_d q[r][h][d] * k[t][d]        over the visible t
+ *   out[r][h][:] = sum_t exp(s[t] - m) v[t][:] / sum_t exp(s[t] - m), m = max s
+ *   lse[r][h] = m + log(sum_t exp(s[t] - m))
+ *
+ * A row with no visible token (length 0) gives out = 0 and lse = -inf. A
+ * length below 0 counts as 0, one beyond table_width * page_size as that; a
+ * token on a page outside [0, n_pages) is not visible. Slots that hold no
+ * visible token are never part of a result, whatever they hold; NaN and
+ * infinities of visible ones go through the formula.
+ *
+ * q, out  device arrays of `dtype` (the cache's, or F16 or BF16 with an
+ *         F8E4M3 cache); element (r, h, d) at r * request_stride +
+ *         h * head_stride + d; any alignment of whole elements. They must not
+ *         overlap. lse: float[n_requests * n_q_heads] or NULL.
+ * table   block table (see above), lengths int32[n_requests].
+ * Scores, maxima, sums and the output's sums are held in 32 bits.
+ * workspace: at least spmv_kv_attention_workspace_size(..) bytes, 16-byte
+ * aligned, zero-filled before its first use and left to this call alone from
+ * then on (each call leaves what the next one needs); calls that may overlap
+ * need one each. The size does not depend on n_requests or lengths.
+ * SPMV_ERR_INVALID_ARG for a bad cache, size, type, overlap, a negative
+ * window or sinks, a scale that is not finite or a short workspace;
+ * SPMV_ERR_UNSUPPORTED when table_width * page_size or n_requests * n_q_heads
+ * passes 2^31 - 1. */
+SPMV_API spmv_status_t spmv_kv_attention_workspace_size(const spmv_kv_cache_t* cache,
+                                                        int32_t n_q_heads, size_t* bytes);
+SPMV_API spmv_status_t spmv_kv_attention(const spmv_kv_cache_t* cache, int64_t n_requests,
+                                         int32_t n_q_heads, const void* q,
+                                         int64_t q_request_stride, int64_t q_head_stride,
+                                         int32_t dtype, const int32_t* table,
+                                         int64_t table_stride, int64_t table_width,
+                                         const int32_t* lengths, double scale, int64_t window,
+                                         int64_t sinks, void* out, int64_t out_request_stride,
+                                         int64_t out_head_stride, float* lse, void* workspace,
+                                         size_t workspace_bytes, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* SPMV_KV_H_ */

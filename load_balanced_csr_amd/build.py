@@ -15,7 +15,9 @@ LIB = os.path.join(HERE, "libspmv.so")
 SOURCES = ["api.hip", "plan_kernels.hip", "merge_kernels.hip", "binned_kernels.hip",
            "probe_kernels.hip", "spmm_kernels.hip", "sort_kernels.hip", "rgcsr_kernels.hip",
            "group_kernels.hip", "noalloc.hip",
-           "tile_kernels.hip", "slab_kernels.hip"]
+           "tile_kernels.hip", "slab_kernels.hip",
+           "kv_api.hip", "kv_table_kernels.hip", "kv_append_kernels.hip",
+           "kv_attention_kernels.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -29,7 +31,7 @@ CFLAGS = [
 
 def _newest_input():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(ROOT, "include", "spmv.h"))
+    files += [os.path.join(ROOT, "include", f) for f in ("spmv.h", "spmv_kv.h")]
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
 

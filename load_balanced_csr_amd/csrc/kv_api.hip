@@ -1,0 +1,398 @@
+// C ABI of the paged-cache operators (declared in include/spmv_kv.h):
+// argument checks and launches. Everything is checked on the host before the
+// first HIP call; lengths, tables and slots, which only the device sees, are
+// checked by the kernels.
+#include "spmv_kv.h"
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+#include "kv_internal.hpp"
+
+namespace spmv {
+// the library's thread-local error text (api.hip)
+void set_last_error(const char* text);
+}  // namespace spmv
+
+namespace {
+
+using namespace spmv;
+
+constexpr int64_t kInt32Max = 2147483647ll;
+
+spmv_status_t fail(spmv_status_t st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+spmv_status_t fail(spmv_status_t st, const char* fmt, ...) {
+  char buf[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  set_last_error(buf);
+  return st;
+}
+
+spmv_status_t launched(hipError_t e, const char* where) {
+  return e == hipSuccess ? SPMV_SUCCESS
+                         : fail(SPMV_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
+}
+
+// The bytes [lo, hi) an array spans (empty: lo == hi).
+struct Span {
+  const char* name;
+  uintptr_t lo, hi;
+};
+Span span(const char* name, const void* p, int64_t bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return Span{name, lo, p && bytes > 0 ? lo + (uintptr_t)bytes : lo};
+}
+bool overlap(const Span& a, const Span& b) {
+  return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
+}
+// Elements from the first to past the last of an array with these sizes and
+// strides (all strides >= 0).
+int64_t extent(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2) {
+  return n0 > 0 && n1 > 0 ? (n0 - 1) * s0 + (n1 - 1) * s1 + n2 : 0;
+}
+
+// Whether rows of n2 elements, n1 of them s1 apart in each of n0 blocks s0
+// apart, lie beside each other.
+bool rows_apart(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2) {
+  return (n1 == 1 || s1 >= n2) && (n0 == 1 || s0 >= extent(1, 0, n1, s1, n2));
+}
+
+int dtype_bytes(int32_t dtype) {
+  switch (dtype) {
+    case SPMV_KV_F32: return 4;
+    case SPMV_KV_F16:
+    case SPMV_KV_BF16: return 2;
+    case SPMV_KV_F8E4M3: return 1;
+  }
+  return 0;
+}
+
+spmv_status_t check_cache(const spmv_kv_cache_t* c) {
+  if (!c) return fail(SPMV_ERR_INVALID_ARG, "cache is NULL");
+  const int eb = dtype_bytes(c->dtype);
+  if (!eb) return fail(SPMV_ERR_INVALID_ARG, "cache dtype %d unknown", c->dtype);
+  if (!c->k || !c->v) return fail(SPMV_ERR_INVALID_ARG, "cache k or v is NULL");
+  if (c->n_pages < 1 || c->page_size < 1 || c->n_heads < 1 || c->head_dim < 1)
+    return fail(SPMV_ERR_INVALID_ARG, "cache sizes must be at least 1");
+  if (c->head_dim > 256)
+    return fail(SPMV_ERR_UNSUPPORTED, "head_dim %d is more than 256", c->head_dim);
+  if ((c->head_dim * eb) % 16)
+    return fail(SPMV_ERR_INVALID_ARG, "head_dim %d is not a multiple of 16 bytes", c->head_dim);
+  if (c->n_pages > kInt32Max / c->page_size)
+    return fail(SPMV_ERR_UNSUPPORTED, "n_pages * page_size beyond int32 slots");
+  const int64_t strides[6] = {c->k_page_stride,  c->k_token_stride, c->k_head_stride,
+                              c->v_page_stride,  c->v_token_stride, c->v_head_stride};
+  for (int64_t s : strides)
+    if (s < 0 || (s * eb) % 16)
+      return fail(SPMV_ERR_INVALID_ARG, "cache strides must be multiples of 16 bytes, not below 0");
+  if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15)
+    return fail(SPMV_ERR_INVALID_ARG, "cache k and v must be 16-byte aligned");
+  if (c->dtype != SPMV_KV_F8E4M3 && (c->k_scale || c->v_scale))
+    return fail(SPMV_ERR_INVALID_ARG, "scales belong to 8-bit caches only");
+  return SPMV_SUCCESS;
+}
+
+Span cache_span(const spmv_kv_cache_t* c, bool values) {
+  const int64_t ps = values ? c->v_page_stride : c->k_page_stride;
+  const int64_t ts = values ? c->v_token_stride : c->k_token_stride;
+  const int64_t hs = values ? c->v_head_stride : c->k_head_stride;
+  const int64_t n = (c->n_pages - 1) * ps + extent(c->page_size, ts, c->n_heads, hs, c->head_dim);
+  return span(values ? "cache v" : "cache k", values ? c->v : c->k, n * dtype_bytes(c->dtype));
+}
+
+// Every output apart from every other array.
+spmv_status_t check_apart(const Span* outs, int n_outs, const Span* ins, int n_ins) {
+  for (int i = 0; i < n_outs; ++i) {
+    for (int j = i + 1; j < n_outs; ++j)
+      if (overlap(outs[i], outs[j]))
+        return fail(SPMV_ERR_INVALID_ARG, "%s and %s overlap", outs[i].name, outs[j].name);
+    for (int j = 0; j < n_ins; ++j)
+      if (overlap(outs[i], ins[j]))
+        return fail(SPMV_ERR_INVALID_ARG, "%s and %s overlap", outs[i].name, ins[j].name);
+  }
+  return SPMV_SUCCESS;
+}
+
+spmv_status_t check_table(int64_t n_requests, int32_t page_size, const void* table,
+                          int64_t table_stride, int64_t table_width) {
+  if (n_requests < 0 || table_width < 0) return fail(SPMV_ERR_INVALID_ARG, "negative size");
+  if (page_size < 1) return fail(SPMV_ERR_INVALID_ARG, "page_size must be at least 1");
+  if (n_requests > 1 && table_stride < table_width)
+    return fail(SPMV_ERR_INVALID_ARG, "table_stride %lld < table_width %lld",
+                (long long)table_stride, (long long)table_width);
+  if (n_requests > kInt32Max || table_width > kInt32Max / page_size)
+    return fail(SPMV_ERR_UNSUPPORTED, "n_requests or table_width * page_size beyond int32");
+  if (n_requests > 0 && table_width > 0 && !table)
+    return fail(SPMV_ERR_INVALID_ARG, "table is NULL");
+  return SPMV_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+spmv_status_t spmv_kv_grow(int64_t n_requests, const int32_t* lengths, const int32_t* n_new,
+                           int32_t page_size, const int32_t* free_pages, int64_t n_free,
+                           const int32_t* cursor, int32_t* table, int64_t table_stride,
+                           int64_t table_width, int32_t* lengths_out, int32_t* cursor_out,
+                           int32_t* token_ptr, int32_t* slots, int32_t* positions,
+                           int64_t n_tokens, int32_t* status, hipStream_t stream) {
+  if (spmv_status_t st = check_table(n_requests, page_size, table, table_stride, table_width))
+    return st;
+  if (n_free < 0 || n_tokens < 0) return fail(SPMV_ERR_INVALID_ARG, "negative size");
+  if (n_free > kInt32Max || n_tokens > kInt32Max)
+    return fail(SPMV_ERR_UNSUPPORTED, "n_free or n_tokens beyond int32");
+  if (!cursor || !cursor_out || !token_ptr || !status ||
+      (n_requests > 0 && (!lengths || !n_new || !lengths_out)) || (n_free > 0 && !free_pages) ||
+      (n_tokens > 0 && !slots))
+    return fail(SPMV_ERR_INVALID_ARG, "NULL array");
+  const Span outs[] = {
+      span("table", table, 4 * extent(n_requests, table_stride, 1, 0, table_width)),
+      span("lengths_out", lengths_out, 4 * n_requests),
+      span("cursor_out", cursor_out, 4),
+      span("token_ptr", token_ptr, 4 * (n_requests + 1)),
+      span("slots", slots, 4 * n_tokens),
+      span("positions", positions, 4 * n_tokens),
+      span("status", status, 8)};
+  const Span ins[] = {span("lengths", lengths, 4 * n_requests),
+                      span("n_new", n_new, 4 * n_requests),
+                      span("free_pages", free_pages, 4 * n_free), span("cursor", cursor, 4)};
+  if (spmv_status_t st = check_apart(outs, 7, ins, 4)) return st;
+
+  KvResizeArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.lengths = lengths;
+  a.arg = n_new;
+  a.cursor = cursor;
+  a.pool = const_cast<int32_t*>(free_pages);
+  a.table = table;
+  a.lengths_out = lengths_out;
+  a.cursor_out = cursor_out;
+  a.token_ptr = token_ptr;
+  a.slots = slots;
+  a.positions = positions;
+  a.status = status;
+  a.table_stride = table_stride;
+  a.table_tokens = (int32_t)(table_width * page_size);
+  a.n_requests = (int32_t)n_requests;
+  a.n_free = (int32_t)n_free;
+  a.n_tokens = (int32_t)n_tokens;
+  a.page = make_fastdiv((uint32_t)page_size);
+  return launched(launch_kv_resize(a, true, stream), "spmv_kv_grow launch");
+}
+
+spmv_status_t spmv_kv_shrink(int64_t n_requests, const int32_t* lengths, const int32_t* keep,
+                             int32_t page_size, int32_t* free_pages, int64_t n_free,
+                             const int32_t* cursor, const int32_t* table, int64_t table_stride,
+                             int64_t table_width, int32_t* lengths_out, int32_t* cursor_out,
+                             int32_t* status, hipStream_t stream) {
+  if (spmv_status_t st = check_table(n_requests, page_size, table, table_stride, table_width))
+    return st;
+  if (n_free < 0) return fail(SPMV_ERR_INVALID_ARG, "negative size");
+  if (n_free > kInt32Max) return fail(SPMV_ERR_UNSUPPORTED, "n_free beyond int32");
+  if (!cursor || !cursor_out || !status ||
+      (n_requests > 0 && (!lengths || !keep || !lengths_out)) || (n_free > 0 && !free_pages))
+    return fail(SPMV_ERR_INVALID_ARG, "NULL array");
+  const Span outs[] = {span("free_pages", free_pages, 4 * n_free),
+                       span("lengths_out", lengths_out, 4 * n_requests),
+                       span("cursor_out", cursor_out, 4), span("status", status, 8)};
+  const Span ins[] = {
+      span("lengths", lengths, 4 * n_requests), span("keep", keep, 4 * n_requests),
+      span("cursor", cursor, 4),
+      span("table", table, 4 * extent(n_requests, table_stride, 1, 0, table_width))};
+  if (spmv_status_t st = check_apart(outs, 4, ins, 4)) return st;
+
+  KvResizeArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.lengths = lengths;
+  a.arg = keep;
+  a.cursor = cursor;
+  a.pool = free_pages;
+  a.table = const_cast<int32_t*>(table);
+  a.lengths_out = lengths_out;
+  a.cursor_out = cursor_out;
+  a.status = status;
+  a.table_stride = table_stride;
+  a.table_tokens = (int32_t)(table_width * page_size);
+  a.n_requests = (int32_t)n_requests;
+  a.n_free = (int32_t)n_free;
+  a.page = make_fastdiv((uint32_t)page_size);
+  return launched(launch_kv_resize(a, false, stream), "spmv_kv_shrink launch");
+}
+
+spmv_status_t spmv_kv_append(const spmv_kv_cache_t* cache, int64_t n_tokens, const void* k,
+                             int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                             int64_t v_token_stride, int64_t v_head_stride, int32_t dtype,
+                             const int32_t* slots, hipStream_t stream) {
+  if (spmv_status_t st = check_cache(cache)) return st;
+  const int eb = dtype_bytes(dtype);
+  if (!eb || dtype == SPMV_KV_F8E4M3 || (dtype != cache->dtype && cache->dtype != SPMV_KV_F8E4M3))
+    return fail(SPMV_ERR_INVALID_ARG, "tokens of dtype %d do not go into a cache of dtype %d",
+                dtype, cache->dtype);
+  if (n_tokens < 0 || k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 ||
+      v_head_stride < 0)
+    return fail(SPMV_ERR_INVALID_ARG, "negative size or stride");
+  if (n_tokens > kInt32Max || (int64_t)cache->n_heads * cache->head_dim * eb / 16 > 32767)
+    return fail(SPMV_ERR_UNSUPPORTED, "more tokens than int32 or rows of more than 524272 bytes");
+  if (n_tokens == 0) return SPMV_SUCCESS;
+  if (!k || !v || !slots) return fail(SPMV_ERR_INVALID_ARG, "NULL array");
+  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % eb)
+    return fail(SPMV_ERR_INVALID_ARG, "k and v must be aligned to their elements");
+  const Span outs[] = {cache_span(cache, false), cache_span(cache, true)};
+  const Span ins[] = {
+      span("k", k, eb * extent(n_tokens, k_token_stride, cache->n_heads, k_head_stride,
+                               cache->head_dim)),
+      span("v", v, eb * extent(n_tokens, v_token_stride, cache->n_heads, v_head_stride,
+                               cache->head_dim)),
+      span("slots", slots, 4 * n_tokens)};
+  // the keys and values of a cache may lie between each other (one array,
+  // strides apart), so only the tokens are held against them
+  for (const Span& o : outs)
+    if (spmv_status_t st = check_apart(&o, 1, ins, 3)) return st;
+
+  KvAppendArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.src[0] = k;
+  a.src[1] = v;
+  a.dst[0] = cache->k;
+  a.dst[1] = cache->v;
+  a.scale[0] = cache->k_scale;
+  a.scale[1] = cache->v_scale;
+  a.src_token[0] = k_token_stride;
+  a.src_token[1] = v_token_stride;
+  a.src_head[0] = k_head_stride;
+  a.src_head[1] = v_head_stride;
+  a.dst_page[0] = cache->k_page_stride;
+  a.dst_page[1] = cache->v_page_stride;
+  a.dst_token[0] = cache->k_token_stride;
+  a.dst_token[1] = cache->v_token_stride;
+  a.dst_head[0] = cache->k_head_stride;
+  a.dst_head[1] = cache->v_head_stride;
+  a.slots = slots;
+  a.n_slots = cache->n_pages * cache->page_size;
+  a.n_tokens = n_tokens;
+  a.n_heads = cache->n_heads;
+  a.head_dim = cache->head_dim;
+  a.src_dtype = dtype;
+  a.dst_dtype = cache->dtype;
+  a.aligned = !(((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) |
+                 (uintptr_t)((k_token_stride | k_head_stride | v_token_stride | v_head_stride) *
+                             eb)) & 15);
+  a.page = make_fastdiv((uint32_t)cache->page_size);
+  return launched(launch_kv_append(a, stream), "spmv_kv_append launch");
+}
+
+static spmv_status_t check_heads(const spmv_kv_cache_t* cache, int32_t n_q_heads) {
+  if (spmv_status_t st = check_cache(cache)) return st;
+  if (n_q_heads < 1 || n_q_heads % cache->n_heads)
+    return fail(SPMV_ERR_INVALID_ARG, "n_q_heads %d is not a multiple of the cache's %d heads",
+                n_q_heads, cache->n_heads);
+  return SPMV_SUCCESS;
+}
+
+spmv_status_t spmv_kv_attention_workspace_size(const spmv_kv_cache_t* cache, int32_t n_q_heads,
+                                               size_t* bytes) {
+  if (!bytes) return fail(SPMV_ERR_INVALID_ARG, "bytes is NULL");
+  if (spmv_status_t st = check_heads(cache, n_q_heads)) return st;
+  *bytes = kv_attention_workspace(cache->n_heads, n_q_heads / cache->n_heads, cache->head_dim);
+  return SPMV_SUCCESS;
+}
+
+spmv_status_t spmv_kv_attention(const spmv_kv_cache_t* cache, int64_t n_requests,
+                                int32_t n_q_heads, const void* q, int64_t q_request_stride,
+                                int64_t q_head_stride, int32_t dtype, const int32_t* table,
+                                int64_t table_stride, int64_t table_width,
+                                const int32_t* lengths, double scale, int64_t window,
+                                int64_t sinks, void* out, int64_t out_request_stride,
+                                int64_t out_head_stride, float* lse, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
+  if (spmv_status_t st = check_heads(cache, n_q_heads)) return st;
+  const int eb = dtype_bytes(dtype);
+  if (!eb || dtype == SPMV_KV_F8E4M3 ||
+      (dtype != cache->dtype && (cache->dtype != SPMV_KV_F8E4M3 || dtype == SPMV_KV_F32)))
+    return fail(SPMV_ERR_INVALID_ARG, "queries of dtype %d do not read a cache of dtype %d",
+                dtype, cache->dtype);
+  if (spmv_status_t st =
+          check_table(n_requests, cache->page_size, table, table_stride, table_width))
+    return st;
+  if (q_request_stride < 0 || q_head_stride < 0 || out_request_stride < 0 || out_head_stride < 0)
+    return fail(SPMV_ERR_INVALID_ARG, "negative stride");
+  if (window < 0 || sinks < 0) return fail(SPMV_ERR_INVALID_ARG, "window or sinks below 0");
+  if (!std::isfinite(scale)) return fail(SPMV_ERR_INVALID_ARG, "scale is not finite");
+  if (n_requests > kInt32Max / n_q_heads)
+    return fail(SPMV_ERR_UNSUPPORTED, "n_requests * n_q_heads beyond int32");
+  if (n_requests == 0) return SPMV_SUCCESS;
+  if (!q || !out || !lengths) return fail(SPMV_ERR_INVALID_ARG, "NULL array");
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) % eb)
+    return fail(SPMV_ERR_INVALID_ARG, "q and out must be aligned to their elements");
+  const int group = n_q_heads / cache->n_heads;
+  const size_t need = kv_attention_workspace(cache->n_heads, group, cache->head_dim);
+  if (workspace_bytes < need || (need && !workspace))
+    return fail(SPMV_ERR_INVALID_ARG, "workspace of %zu bytes needed, %zu given", need,
+                workspace ? workspace_bytes : 0);
+  if (reinterpret_cast<uintptr_t>(workspace) & 15)
+    return fail(SPMV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  const int64_t q_extent =
+      extent(n_requests, q_request_stride, n_q_heads, q_head_stride, cache->head_dim);
+  const int64_t out_extent =
+      extent(n_requests, out_request_stride, n_q_heads, out_head_stride, cache->head_dim);
+  const Span outs[] = {span("out", out, eb * out_extent),
+                       span("lse", lse, 4 * n_requests * n_q_heads),
+                       span("workspace", workspace, (int64_t)need)};
+  const Span ins[] = {span("q", q, eb * q_extent), cache_span(cache, false),
+                      cache_span(cache, true),
+                      span("table", table, 4 * extent(n_requests, table_stride, 1, 0, table_width)),
+                      span("lengths", lengths, 4 * n_requests)};
+  if (spmv_status_t st = check_apart(outs, 3, ins, 5)) return st;
+  // rows of out that share elements would be written by several workgroups
+  if (!rows_apart(n_requests, out_request_stride, n_q_heads, out_head_stride, cache->head_dim) &&
+      !rows_apart(n_q_heads, out_head_stride, n_requests, out_request_stride, cache->head_dim))
+    return fail(SPMV_ERR_INVALID_ARG, "rows of out overlap");
+
+  KvAttentionArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.k = cache->k;
+  a.v = cache->v;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.table = table;
+  a.lengths = lengths;
+  a.workspace = workspace;
+  a.q_request = q_request_stride;
+  a.q_head = q_head_stride;
+  a.out_request = out_request_stride;
+  a.out_head = out_head_stride;
+  a.k_page = cache->k_page_stride;
+  a.k_token = cache->k_token_stride;
+  a.k_head = cache->k_head_stride;
+  a.v_page = cache->v_page_stride;
+  a.v_token = cache->v_token_stride;
+  a.v_head = cache->v_head_stride;
+  a.table_stride = table_stride;
+  a.table_tokens = (int32_t)(table_width * cache->page_size);
+  a.n_pages = (int32_t)cache->n_pages;
+  a.n_requests = (int32_t)n_requests;
+  a.n_kv_heads = cache->n_heads;
+  a.group = group;
+  a.head_dim = cache->head_dim;
+  // a window of at least the longest row is none
+  a.window = window >= a.table_tokens ? 0 : (int32_t)window;
+  a.sinks = (int32_t)(sinks < kInt32Max ? sinks : kInt32Max);
+  a.cache_dtype = cache->dtype;
+  a.dtype = dtype;
+  a.scale = (float)scale;
+  a.page = make_fastdiv((uint32_t)cache->page_size);
+  return launched(launch_kv_attention(a, stream), "spmv_kv_attention launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,101 @@
+// New keys and values to their slots (spmv_kv_append): a scatter of whole
+// rows of head_dim elements, bound by copy bandwidth (each element is read
+// and written once) and, for the few tokens of a decoding step, by latency.
+// One thread per 16 bytes of k and of v; keys and values in one launch.
+#include <hip/hip_runtime.h>
+
+#include "device_common.hpp"
+#include "kv_internal.hpp"
+#include "kv_types.hpp"
+
+namespace spmv {
+namespace {
+
+// S: type of the new tokens, T: type of the cache. VEC elements per thread
+// (16 bytes of S); T's share of a vector is a whole number of 32-bit words.
+template <typename S, typename T, bool ALIGNED>
+__global__ __launch_bounds__(kBlock) void kv_append_kernel(KvAppendArgs a, uint32_t vecs_per_head,
+                                                           FastDiv by_token, FastDiv by_head) {
+  constexpr int VEC = 16 / sizeof(S);
+  const uint32_t i = blockIdx.x * kBlock + threadIdx.x;   // vector of this block row's tokens
+  const uint32_t t_in = div_by(i, by_token);              // token within the block row
+  const int64_t t = (int64_t)blockIdx.y * 65536 + t_in;
+  if (t_in >= 65536 || t >= a.n_tokens) return;
+  const int32_t slot = a.slots[t];
+  if (slot < 0 || slot >= a.n_slots) return;
+  const uint32_t rest = i - t_in * by_token.d;
+  const uint32_t head = div_by(rest, by_head);
+  const int64_t d = (int64_t)(rest - head * vecs_per_head) * VEC;
+  const uint32_t page = div_by((uint32_t)slot, a.page);
+  const uint32_t in_page = (uint32_t)slot - page * a.page.d;
+
+  alignas(16) S x[2][VEC];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const S* p = static_cast<const S*>(a.src[w]) + t * a.src_token[w] + head * a.src_head[w] + d;
+    if (ALIGNED) {
+      *reinterpret_cast<u32x4*>(x[w]) = *reinterpret_cast<const u32x4*>(p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[w][e] = p[e];
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    T* p = static_cast<T*>(a.dst[w]) + page * a.dst_page[w] + in_page * a.dst_token[w] +
+           head * a.dst_head[w] + d;
+    if constexpr (sizeof(T) == sizeof(S)) {
+      *reinterpret_cast<u32x4*>(p) = *reinterpret_cast<const u32x4*>(x[w]);
+    } else {
+      const float scale = a.scale[w] ? a.scale[w][head] : 1.f;
+      uint32_t word[VEC / 4];
+#pragma unroll
+      for (int g = 0; g < VEC / 4; ++g) {
+        word[g] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          word[g] |= (uint32_t)from_f32<f8>(to_f32(x[w][4 * g + e]) / scale).bits << (8 * e);
+      }
+#pragma unroll
+      for (int g = 0; g < VEC / 4; ++g) reinterpret_cast<uint32_t*>(p)[g] = word[g];
+    }
+  }
+}
+
+template <typename S, typename T>
+hipError_t launch_append(const KvAppendArgs& a, hipStream_t s) {
+  const uint32_t vph = a.head_dim / (16 / sizeof(S));
+  const uint32_t vpt = vph * a.n_heads;
+  // a block row holds up to 65536 tokens: vector numbers stay in 31 bits for
+  // every token of up to 32767 vectors
+  const int64_t rows = (a.n_tokens + 65535) / 65536;
+  const int64_t per_row = a.n_tokens < 65536 ? a.n_tokens : 65536;
+  if (vpt > 32767 || rows > 65535) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)((per_row * vpt + kBlock - 1) / kBlock), (unsigned)rows);
+  const FastDiv by_token = make_fastdiv(vpt), by_head = make_fastdiv(vph);
+  if (a.aligned)
+    hipLaunchKernelGGL((kv_append_kernel<S, T, true>), grid, dim3(kBlock), 0, s, a, vph, by_token,
+                       by_head);
+  else
+    hipLaunchKernelGGL((kv_append_kernel<S, T, false>), grid, dim3(kBlock), 0, s, a, vph,
+                       by_token, by_head);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t s) {
+  if (a.dst_dtype == SPMV_KV_F8E4M3) {
+    switch (a.src_dtype) {
+      case SPMV_KV_F32: return launch_append<float, f8>(a, s);
+      case SPMV_KV_F16: return launch_append<f16, f8>(a, s);
+      case SPMV_KV_BF16: return launch_append<bf16, f8>(a, s);
+    }
+    return hipErrorInvalidValue;
+  }
+  // the same type on both sides: words are moved, whatever they mean
+  return a.dst_dtype == SPMV_KV_F32 ? launch_append<float, float>(a, s)
+                                    : launch_append<f16, f16>(a, s);
+}
+
+}  // namespace spmv

@@ -1,0 +1,238 @@
+// Block tables and slot maps from request lengths (spmv_kv_grow), and pages
+// back to the pool (spmv_kv_shrink).
+//
+// Both are an exclusive scan over the requests (pages, and for growth new
+// tokens) followed by independent writes, one per page and one per token, at
+// places the scan fixes. What bounds them is latency: one launch, the loads
+// of lengths, the scan, the loads of pages, the stores. So there is one
+// launch with no hand-off between workgroups: every workgroup scans all
+// requests by itself (two int32 per request, read from L2 by all but the
+// first) and then takes its share of the pages and tokens. A scan shared
+// through memory would cost a second launch or a wait.
+//
+// The scan is over chunks of rows, one per thread: the chunks' prefix sums
+// stay in LDS, and a page or token finds its row by a binary search over
+// the 1024 chunks and then a walk inside one (no walk up to 1024 requests).
+// All sums are 64-bit until the checks have shown that they fit 31 bits.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "device_common.hpp"
+#include "kv_internal.hpp"
+
+namespace spmv {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWaves = kThreads / kWave;
+// Tokens per workgroup at which one more workgroup is launched.
+constexpr int kTokensPerBlock = 4 * kThreads;
+constexpr int kMaxBlocks = 256;
+
+struct Counts {
+  int64_t pages, tokens;
+};
+
+struct Row {
+  int32_t first;    // pages kept as they are: held (grow), ceil(keep / P) (shrink)
+  int32_t pages;    // pages that move
+  int32_t tokens;   // new tokens (grow)
+  bool bad;
+};
+
+template <bool GROW>
+__device__ __forceinline__ Row row_counts(const KvResizeArgs& a, int r) {
+  const int32_t len = a.lengths[r], arg = a.arg[r];
+  Row x;
+  if (GROW) {
+    x.bad = len < 0 || arg < 0 || (int64_t)len + arg > a.table_tokens;
+  } else {
+    x.bad = arg < 0 || arg > len || len > a.table_tokens;
+  }
+  if (x.bad) {
+    x.first = x.pages = x.tokens = 0;
+    return x;
+  }
+  // ceil(n / P) = (n + P - 1) / P needs n + P - 1 < 2^31; n - 1 does not
+  auto pages_of = [&](int32_t n) {
+    return n > 0 ? (int32_t)div_by((uint32_t)n - 1, a.page) + 1 : 0;
+  };
+  const int32_t before = pages_of(GROW ? len : arg);
+  x.first = before;
+  x.pages = pages_of(GROW ? len + arg : len) - before;
+  x.tokens = GROW ? arg : 0;
+  return x;
+}
+
+// The last chunk whose prefix is <= i, among n_chunks (prefix[0] = 0).
+__device__ __forceinline__ int find_chunk(const int32_t* prefix, int n_chunks, int32_t i) {
+  int lo = 0, hi = n_chunks - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= i)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+template <bool GROW>
+__global__ __launch_bounds__(kThreads) void kv_resize_kernel(KvResizeArgs a) {
+  __shared__ int64_t wave_pages[kWaves], wave_tokens[kWaves];
+  __shared__ int32_t wave_bad[kWaves];
+  __shared__ int32_t page_prefix[kThreads], token_prefix[kThreads];
+
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
+  const int R = a.n_requests;
+  const int per = max(1, (R + kThreads - 1) / kThreads);  // rows per chunk
+  const int n_chunks = (R + per - 1) / per;
+  const int r0 = tid * per, r1 = min(R, r0 + per);
+  const int32_t cursor = min(max(a.cursor[0], 0), a.n_free);
+
+  Counts sum{0, 0};
+  int32_t bad = INT_MAX;
+  for (int r = r0; r < r1; ++r) {
+    const Row x = row_counts<GROW>(a, r);
+    sum.pages += x.pages;
+    sum.tokens += x.tokens;
+    if (x.bad && bad == INT_MAX) bad = r;
+  }
+  Counts incl = sum;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int64_t p = __shfl_up(incl.pages, d), t = __shfl_up(incl.tokens, d);
+    if (lane >= d) {
+      incl.pages += p;
+      incl.tokens += t;
+    }
+    bad = min(bad, __shfl_xor(bad, d));
+  }
+  if (lane == kWave - 1) {
+    wave_pages[wave] = incl.pages;
+    wave_tokens[wave] = incl.tokens;
+    wave_bad[wave] = bad;
+  }
+  __syncthreads();
+  Counts before{0, 0}, total{0, 0};
+  bad = INT_MAX;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w == wave) before = total;
+    total.pages += wave_pages[w];
+    total.tokens += wave_tokens[w];
+    bad = min(bad, wave_bad[w]);
+  }
+  // exclusive prefix of this thread's chunk
+  before.pages += incl.pages - sum.pages;
+  before.tokens += incl.tokens - sum.tokens;
+
+  const int64_t avail = GROW ? a.n_free - cursor : cursor;
+  int32_t code = SPMV_KV_OK;
+  int64_t detail = 0;
+  if (bad != INT_MAX) {
+    code = SPMV_KV_BAD_ROW;
+    detail = bad;
+  } else if (GROW && total.tokens > a.n_tokens) {
+    code = SPMV_KV_NO_ROOM;
+    detail = total.tokens;
+  } else if (total.pages > avail) {
+    code = SPMV_KV_NO_PAGES;
+    detail = total.pages - avail;
+  }
+  const bool ok = code == SPMV_KV_OK;
+
+  if (blockIdx.x == 0) {
+    int64_t at = before.tokens;
+    for (int r = r0; r < r1; ++r) {
+      if (GROW) {
+        a.token_ptr[r] = (int32_t)min(at, (int64_t)INT_MAX);
+        at += row_counts<true>(a, r).tokens;
+      }
+      a.lengths_out[r] = ok ? (GROW ? a.lengths[r] + a.arg[r] : a.arg[r]) : a.lengths[r];
+    }
+    if (tid == 0) {
+      if (GROW) a.token_ptr[R] = (int32_t)min(total.tokens, (int64_t)INT_MAX);
+      const int32_t moved = ok ? (int32_t)total.pages : 0;
+      a.cursor_out[0] = GROW ? cursor + moved : cursor - moved;
+      a.status[0] = code;
+      a.status[1] = (int32_t)min(detail, (int64_t)INT_MAX);
+    }
+  }
+  const int stride = gridDim.x * kThreads, first = blockIdx.x * kThreads + tid;
+  if (!ok) {
+    if (GROW)
+      for (int64_t t = first; t < a.n_tokens; t += stride) {
+        a.slots[t] = -1;
+        if (a.positions) a.positions[t] = -1;
+      }
+    return;
+  }
+  // from here every sum fits 31 bits: pages <= n_free, tokens <= n_tokens
+  page_prefix[tid] = (int32_t)before.pages;
+  token_prefix[tid] = (int32_t)before.tokens;
+  __syncthreads();
+
+  const int32_t base = GROW ? cursor : cursor - (int32_t)total.pages;
+  for (int64_t i = first; i < total.pages; i += stride) {
+    const int c = find_chunk(page_prefix, n_chunks, (int32_t)i);
+    int32_t j = (int32_t)i - page_prefix[c];
+    int r = c * per;
+    Row x = row_counts<GROW>(a, r);
+    while (j >= x.pages) {
+      j -= x.pages;
+      x = row_counts<GROW>(a, ++r);
+    }
+    int32_t* entry = a.table + (int64_t)r * a.table_stride + x.first + j;
+    int32_t* page = a.pool + base + i;
+    if (GROW)
+      *entry = *page;
+    else
+      *page = *entry;
+  }
+  if (!GROW) return;
+
+  for (int64_t t = first; t < a.n_tokens; t += stride) {
+    int32_t slot = -1, pos = -1;
+    if (t < total.tokens) {
+      const int c = find_chunk(token_prefix, n_chunks, (int32_t)t);
+      int32_t i = (int32_t)t - token_prefix[c], pages = page_prefix[c];
+      int r = c * per;
+      Row x = row_counts<GROW>(a, r);
+      while (i >= x.tokens) {
+        i -= x.tokens;
+        pages += x.pages;
+        x = row_counts<GROW>(a, ++r);
+      }
+      pos = a.lengths[r] + i;
+      const int32_t j = (int32_t)div_by((uint32_t)pos, a.page);
+      // a page this call hands out is read from the pool: the table entry
+      // may not be written yet
+      const int32_t page = j < x.first ? a.table[(int64_t)r * a.table_stride + j]
+                                       : a.pool[cursor + pages + j - x.first];
+      const int64_t s = (int64_t)page * a.page.d + (pos - j * (int32_t)a.page.d);
+      slot = page < 0 || s > INT_MAX ? -1 : (int32_t)s;
+    }
+    a.slots[t] = slot;
+    if (a.positions) a.positions[t] = pos;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_kv_resize(const KvResizeArgs& a, bool grow, hipStream_t s) {
+  // one workgroup per kTokensPerBlock tokens; a shrink's pages are not known
+  // here, so it is sized by its requests
+  const int64_t work = grow ? (int64_t)a.n_tokens : (int64_t)a.n_requests * 8;
+  const int blocks =
+      (int)std::min<int64_t>(kMaxBlocks, std::max<int64_t>(1, work / kTokensPerBlock));
+  if (grow)
+    hipLaunchKernelGGL(kv_resize_kernel<true>, dim3(blocks), dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL(kv_resize_kernel<false>, dim3(blocks), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace spmv

@@ -1,0 +1,311 @@
+"""Paged key-value caches (the C ABI in include/spmv_kv.h): block tables and
+slot maps built on the GPU from request lengths, new keys and values written
+to their slots, and the attention of one new token per request.
+
+Argument marshalling only, as in binding.py: tensors become pointers, sizes
+and strides, their lengths are checked here, the current torch stream becomes
+the hipStream_t, statuses become SpmvError.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import binding
+from .binding import _check, _stream
+
+KV_F32, KV_F16, KV_BF16, KV_F8E4M3 = 0, 1, 2, 3
+KV_DTYPE = {torch.float32: KV_F32, torch.float16: KV_F16, torch.bfloat16: KV_BF16,
+            torch.float8_e4m3fn: KV_F8E4M3}
+KV_OK, KV_NO_PAGES, KV_BAD_ROW, KV_NO_ROOM = 0, 1, 2, 3
+
+KV_EXPORTED = ("spmv_kv_grow", "spmv_kv_shrink", "spmv_kv_append",
+               "spmv_kv_attention_workspace_size", "spmv_kv_attention")
+
+
+class KvCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("k_page_stride", ctypes.c_int64),
+                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_page_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
+                ("v_head_stride", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+_lib = None
+
+
+def _load():
+    global _lib
+    if _lib is None:
+        lib = binding.load()
+        i64, i32, p, d = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_double
+        lib.spmv_kv_grow.argtypes = [i64, p, p, i32, p, i64, p, p, i64, i64, p, p, p, p, p, i64,
+                                     p, p]
+        lib.spmv_kv_shrink.argtypes = [i64, p, p, i32, p, i64, p, p, i64, i64, p, p, p, p]
+        lib.spmv_kv_append.argtypes = [p, i64, p, i64, i64, p, i64, i64, i32, p, p]
+        lib.spmv_kv_attention_workspace_size.argtypes = [p, i32, p]
+        lib.spmv_kv_attention.argtypes = [p, i64, i32, p, i64, i64, i32, p, i64, i64, p, d, i64,
+                                          i64, p, i64, i64, p, p, ctypes.c_size_t, p]
+        for name in KV_EXPORTED:
+            getattr(lib, name).restype = ctypes.c_int
+        _lib = lib
+    return _lib
+
+
+def _ints(t, name: str, n: int) -> int:
+    """Pointer of a contiguous device int32 tensor of at least n entries."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        raise TypeError("%s must be an int32 tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a device (cuda) tensor" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.numel() < n:
+        raise ValueError("%s has %d entries, %d are needed" % (name, t.numel(), n))
+    return t.data_ptr()
+
+
+def _table(t, n_requests: int):
+    """Pointer, row stride and width of a block table of n_requests rows."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        raise TypeError("table must be an int32 tensor")
+    if not t.is_cuda:
+        raise ValueError("table must be a device (cuda) tensor")
+    if t.dim() != 2 or t.shape[0] < n_requests or (t.stride(1) != 1 and t.shape[1] > 1 and
+                                                   t.numel()):
+        raise ValueError("table must be 2-D with %d rows and a unit column stride" % n_requests)
+    return t.data_ptr(), t.stride(0), t.shape[1]
+
+
+def _on(stream):
+    """Context in which tensors are made for `stream` (the current one if None), so that
+    their memory and first fill are ordered with the calls on it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _rows(t, name: str, shape):
+    """Pointer and the two outer strides of a device tensor [n, heads, head_dim] with a
+    unit last stride; a size that is None may be anything."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a device (cuda) tensor" % name)
+    if t.dim() != 3 or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError("%s must have shape %s, not %s"
+                         % (name, tuple("*" if w is None else w for w in shape), tuple(t.shape)))
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and t.shape[2] > 1:
+        raise ValueError("%s must have a unit last stride" % name)
+    return t.data_ptr(), s0, s1
+
+
+def spmv_kv_grow(lengths, n_new, page_size: int, free_pages, cursor, table, lengths_out,
+                 cursor_out, token_ptr, slots, positions, status, stream=None) -> None:
+    """Pages for n_new[r] tokens more of each request, taken from free_pages from cursor on
+    and entered in the block table; the tokens' CSR offsets, slots and positions. The
+    number of requests is lengths.numel(), the room for tokens slots.numel() (the entries
+    past the last token become -1); positions may be None. All or nothing: status[0] tells
+    (KV_OK, KV_NO_PAGES, KV_BAD_ROW, KV_NO_ROOM). Asynchronous; every output is an array
+    of its own."""
+    n = lengths.numel()
+    n_tokens = slots.numel()
+    tp, ts, tw = _table(table, n)
+    _check(_load().spmv_kv_grow(
+        n, _ints(lengths, "lengths", n), _ints(n_new, "n_new", n), page_size,
+        _ints(free_pages, "free_pages", 0), free_pages.numel(), _ints(cursor, "cursor", 1),
+        tp, ts, tw, _ints(lengths_out, "lengths_out", n), _ints(cursor_out, "cursor_out", 1),
+        _ints(token_ptr, "token_ptr", n + 1), _ints(slots, "slots", 0),
+        None if positions is None else _ints(positions, "positions", n_tokens), n_tokens,
+        _ints(status, "status", 2), _stream(stream)), "spmv_kv_grow")
+
+
+def spmv_kv_shrink(lengths, keep, page_size: int, free_pages, cursor, table, lengths_out,
+                   cursor_out, status, stream=None) -> None:
+    """The pages past keep[r] <= lengths[r] tokens of each request back to the pool (they
+    become free_pages[cursor_out] .. free_pages[cursor - 1]). Status and the rest as for
+    spmv_kv_grow."""
+    n = lengths.numel()
+    tp, ts, tw = _table(table, n)
+    _check(_load().spmv_kv_shrink(
+        n, _ints(lengths, "lengths", n), _ints(keep, "keep", n), page_size,
+        _ints(free_pages, "free_pages", 0), free_pages.numel(), _ints(cursor, "cursor", 1),
+        tp, ts, tw, _ints(lengths_out, "lengths_out", n), _ints(cursor_out, "cursor_out", 1),
+        _ints(status, "status", 2), _stream(stream)), "spmv_kv_shrink")
+
+
+class KvCache:
+    """One layer's paged cache over borrowed tensors ``k`` and ``v`` of shape
+    [n_pages, page_size, n_kv_heads, head_dim] (float32, float16, bfloat16 or
+    float8_e4m3fn), any strides with a unit last one: a pool stored
+    [n_pages, n_kv_heads, page_size, head_dim] is passed as its transpose(1, 2).
+    8-bit caches take float32 scales per head. The cache keeps a workspace of the
+    attention for each stream it was called on."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        for t, name in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("%s must be a torch tensor" % name)
+            if t.dtype not in KV_DTYPE:
+                raise TypeError("%s has dtype %s, expected one of %s"
+                                % (name, t.dtype, tuple(KV_DTYPE)))
+            if not t.is_cuda:
+                raise ValueError("%s must be a device (cuda) tensor" % name)
+            if t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] > 1):
+                raise ValueError("%s must be [n_pages, page_size, n_kv_heads, head_dim] with a "
+                                 "unit last stride" % name)
+        if k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must have the same shape, dtype and device")
+        self.n_pages, self.page_size, self.n_heads, self.head_dim = k.shape
+        self.dtype, self.device = k.dtype, k.device
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is None:
+                continue
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+                raise TypeError("%s must be a float32 tensor" % name)
+            if t.device != k.device or not t.is_contiguous() or t.numel() != self.n_heads:
+                raise ValueError("%s must be a contiguous tensor of %d values on the cache's "
+                                 "device" % (name, self.n_heads))
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._struct = KvCacheStruct(
+            k.data_ptr(), v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+            None if v_scale is None else v_scale.data_ptr(), self.n_pages, *k.stride()[:3],
+            *v.stride()[:3], self.page_size, self.n_heads, self.head_dim, KV_DTYPE[k.dtype])
+        self._ref = ctypes.addressof(self._struct)
+        self._need: dict = {}
+        self._ws: dict = {}                 # stream handle -> workspace
+
+    def append(self, k, v, slots, stream=None) -> None:
+        """Write k[t], v[t] ([n_tokens, n_kv_heads, head_dim]) to slot slots[t] for every
+        token; slots outside the cache (-1) are skipped."""
+        kp, k0, k1 = _rows(k, "k", (None, self.n_heads, self.head_dim))
+        vp, v0, v1 = _rows(v, "v", k.shape)
+        if k.dtype != v.dtype or k.dtype not in KV_DTYPE:
+            raise TypeError("k and v must have one dtype of %s" % (tuple(KV_DTYPE),))
+        n = k.shape[0]
+        _check(_load().spmv_kv_append(self._ref, n, kp, k0, k1, vp, v0, v1, KV_DTYPE[k.dtype],
+                                      _ints(slots, "slots", n), _stream(stream)),
+               "spmv_kv_append")
+
+    def workspace_size(self, n_q_heads: int) -> int:
+        """Bytes of workspace attend() needs; the tensor given must be zero-filled once."""
+        need = self._need.get(n_q_heads)
+        if need is None:
+            b = ctypes.c_size_t(0)
+            _check(_load().spmv_kv_attention_workspace_size(self._ref, n_q_heads,
+                                                            ctypes.addressof(b)),
+                   "spmv_kv_attention_workspace_size")
+            need = self._need[n_q_heads] = int(b.value)
+        return need
+
+    def attend(self, q, table, lengths, out=None, scale: Optional[float] = None, window: int = 0,
+               sinks: int = 0, lse=None, workspace=None, stream=None):
+        """softmax(scale * q k^T) v of one token per request: q and out
+        [n_requests, n_q_heads, head_dim], table the block table, lengths int32 with the
+        newest token counted. window 0 sees every token, otherwise the last ``window`` and
+        the first ``sinks``. scale: head_dim ** -0.5 unless given. lse: float32
+        [n_requests, n_q_heads] to receive the log of the softmax's sum. Returns out."""
+        qp, q0, q1 = _rows(q, "q", (None, None, self.head_dim))
+        n, heads = q.shape[0], q.shape[1]
+        if out is None:
+            with _on(stream):
+                out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        op, o0, o1 = _rows(out, "out", q.shape)
+        if q.dtype not in KV_DTYPE or out.dtype != q.dtype:
+            raise TypeError("q and out must have one dtype of %s" % (tuple(KV_DTYPE),))
+        tp, ts, tw = _table(table, n)
+        lp = None
+        if lse is not None:
+            if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32:
+                raise TypeError("lse must be a float32 tensor")
+            if not lse.is_cuda or not lse.is_contiguous() or lse.numel() != n * heads:
+                raise ValueError("lse must be a contiguous device tensor of %d values"
+                                 % (n * heads))
+            lp = lse.data_ptr()
+        need = self.workspace_size(heads)
+        handle = _stream(stream)
+        if workspace is None:
+            workspace = self._ws.get(handle)
+            if workspace is None or workspace.numel() < need:
+                with _on(stream):
+                    workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
+                self._ws[handle] = workspace
+        elif not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous device tensor")
+        _check(_load().spmv_kv_attention(
+            self._ref, n, heads, qp, q0, q1, KV_DTYPE[q.dtype], tp, ts, tw,
+            _ints(lengths, "lengths", n), self.head_dim ** -0.5 if scale is None else scale,
+            window, sinks, op, o0, o1, lp, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), handle), "spmv_kv_attention")
+        return out
+
+
+class PageTable:
+    """The block table, lengths and page pool of a batch of n_requests rows, kept on the
+    device: ``grow`` before a step's tokens are appended, ``shrink`` when requests end or
+    lose their last tokens (keep 0 ends one; its row can then take a new request). Both
+    are asynchronous; ``status`` reads back how the last one went."""
+
+    def __init__(self, n_requests: int, max_pages: int, n_pages: int, page_size: int,
+                 device="cuda"):
+        def ints(*shape, fill=0):
+            return torch.full(shape, fill, dtype=torch.int32, device=device)
+
+        self.page_size = int(page_size)
+        self.table = ints(n_requests, max_pages, fill=-1)
+        self.free_pages = torch.arange(n_pages, dtype=torch.int32, device=device)
+        self.token_ptr = ints(n_requests + 1)
+        # two of each: a call reads one and writes the other
+        self._lengths = (ints(n_requests), ints(n_requests))
+        self._cursor = (ints(1), ints(1))
+        self._status = ints(2)
+        self._now = 0
+
+    @property
+    def lengths(self):
+        """int32 tokens of each request, as the last grow or shrink left them."""
+        return self._lengths[self._now]
+
+    @property
+    def cursor(self):
+        """int32[1]: pages in use."""
+        return self._cursor[self._now]
+
+    @property
+    def status(self):
+        """(code, detail) of the last call; waits for it."""
+        code, detail = self._status.tolist()
+        return code, detail
+
+    def grow(self, n_new, n_tokens: int, slots=None, positions=None, stream=None):
+        """Room for n_new[r] (int32, device) tokens more of each request, n_tokens in all
+        at most (slots.numel(), if slots is given). Returns their slots and positions, -1 past the last; ``token_ptr`` says
+        which are whose."""
+        with _on(stream):
+            if slots is None:
+                slots = torch.empty(n_tokens, dtype=torch.int32, device=self.table.device)
+            if positions is None:
+                positions = torch.empty(n_tokens, dtype=torch.int32, device=self.table.device)
+        now, then = self._now, 1 - self._now
+        spmv_kv_grow(self._lengths[now], n_new, self.page_size, self.free_pages,
+                     self._cursor[now], self.table, self._lengths[then], self._cursor[then],
+                     self.token_ptr, slots, positions, self._status, stream)
+        self._now = then
+        return slots, positions
+
+    def shrink(self, keep, stream=None) -> None:
+        """Keep the first keep[r] (int32, device) tokens of each request."""
+        now, then = self._now, 1 - self._now
+        spmv_kv_shrink(self._lengths[now], keep, self.page_size, self.free_pages,
+                       self._cursor[now], self.table, self._lengths[then], self._cursor[then],
+                       self._status, stream)
+        self._now = then

@@ -1,0 +1,199 @@
+"""spmv_kv_grow and spmv_kv_shrink against a plain loop: whole numbers, so
+every output has to be equal, over odd sizes, failing calls and chains of
+steps."""
+import numpy as np
+import pytest
+import torch
+
+import load_balanced_csr_amd as lb
+import kv_ref
+
+pytestmark = pytest.mark.gpu
+
+
+def dev(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+
+
+def run_grow(lengths, n_new, page, free, cursor, table, n_tokens, positions=True, width=None):
+    R = len(lengths)
+    wide = dev(table)
+    t = wide if width is None else wide[:, :width]
+    lo, co, tp, st = dev([7] * R), dev([7]), dev([7] * (R + 1)), dev([7, 7])
+    slots, pos = dev([7] * n_tokens), dev([7] * n_tokens) if positions else None
+    ins = dev(lengths), dev(n_new), dev(free), dev([cursor])
+    lb.spmv_kv_grow(ins[0], ins[1], page, ins[2], ins[3], t, lo, co, tp, slots, pos, st)
+    torch.cuda.synchronize()
+    assert ins[2].tolist() == list(free) and ins[3].tolist() == [cursor]
+    return (wide.cpu().numpy(), lo.tolist(), int(co), tp.tolist(), slots.tolist(),
+            pos.tolist() if positions else None, tuple(st.tolist()))
+
+
+def check_grow(lengths, n_new, page, free, cursor, table, n_tokens):
+    want = kv_ref.grow(lengths, n_new, page, free, cursor, table, n_tokens)
+    got = run_grow(lengths, n_new, page, free, cursor, table, n_tokens)
+    assert np.array_equal(got[0], want[0])
+    assert got[1:] == tuple(want[1:])
+    return want
+
+
+def batch(rng, R, page, longest, width):
+    """Lengths, a table that holds them and the pages left, in a random order."""
+    lengths = rng.integers(0, longest + 1, R)
+    held = [kv_ref.pages_of(int(n), page) for n in lengths]
+    pool = rng.permutation(sum(held) + 4 * R + 8)
+    table = np.full((R, width), -1, dtype=np.int64)
+    at = 0
+    for r, h in enumerate(held):
+        table[r, :h] = pool[at:at + h]
+        at += h
+    return [int(n) for n in lengths], table, [int(p) for p in pool], at
+
+
+@pytest.mark.parametrize("R", [1, 2, 63, 64, 65, 500, 1023, 1024, 1025, 2500])
+@pytest.mark.parametrize("page", [1, 7, 16, 100])
+def test_grow(R, page):
+    rng = np.random.default_rng(R * 1000 + page)
+    lengths, table, pool, used = batch(rng, R, page, 3 * page, 8)
+    n_new = [int(n) for n in rng.integers(0, 2 * page + 1, R)]
+    want = check_grow(lengths, n_new, page, pool, used, table, sum(n_new) + 5)
+    assert want[-1] == (0, 0)
+
+
+def test_grow_one_token_of_each_request():
+    rng = np.random.default_rng(1)
+    lengths, table, pool, used = batch(rng, 300, 16, 1000, 70)
+    assert check_grow(lengths, [1] * 300, 16, pool, used, table, 300)[-1] == (0, 0)
+
+
+def test_grow_prompts_over_several_workgroups():
+    rng = np.random.default_rng(2)
+    R, page = 37, 16
+    n_new = [int(n) for n in rng.integers(0, 2000, R)]
+    pool = [int(p) for p in rng.permutation(sum(n_new) // page + R)]
+    table = np.full((R, 130), -1, dtype=np.int64)
+    assert check_grow([0] * R, n_new, page, pool, 0, table, sum(n_new))[-1] == (0, 0)
+    # rows that take nothing between rows that do
+    n_new = [0 if r % 3 else 1500 for r in range(R)]
+    assert check_grow([0] * R, n_new, page, pool, 0, table, 40000)[-1] == (0, 0)
+
+
+def test_grow_nothing():
+    check_grow([], [], 16, [1, 2], 1, np.zeros((0, 4), dtype=np.int64), 3)
+    check_grow([0, 5], [0, 0], 16, [4, 2], 1, np.full((2, 2), 3), 0)
+    check_grow([0, 5], [0, 0], 16, [], 0, np.full((2, 2), 3), 9)
+
+
+@pytest.mark.parametrize("case,code", [
+    (dict(n_new=[1, 17, 1], free=[5, 6], n_tokens=19), 1),   # three pages from two
+    (dict(cursor=40), 1),                                  # a cursor past the pool's end
+    (dict(n_new=[1, -1, 1]), 2), (dict(lengths=[3, 3, -3]), 2),
+    (dict(n_new=[1, 62, 1]), 2),                           # more than the table row holds
+    (dict(n_new=[1, 2147483647, 2147483647]), 2),
+    (dict(n_tokens=2), 3)])
+def test_grow_is_all_or_nothing(case, code):
+    a = dict(lengths=[0, 3, 16], n_new=[1, 1, 1], page=16, free=[9, 8, 7, 6], cursor=0,
+             table=np.arange(12).reshape(3, 4), n_tokens=6)
+    a.update(case)
+    want = check_grow(*a.values())
+    assert want[-1][0] == code and set(want[4]) == {-1}
+
+
+def test_grow_with_a_cursor_below_zero_and_pages_without_a_slot():
+    check_grow([0], [3], 4, [9, 8], -5, np.full((1, 2), -1), 3)
+    got = run_grow([0, 4], [3, 1], 4, [-1, 2 ** 31 - 1], 0, np.full((2, 2), 5), 4)
+    assert got[4] == [-1] * 4 and got[5] == [0, 1, 2, 4] and got[6] == (0, 0)
+
+
+def test_grow_without_positions_and_with_a_wider_table():
+    a = ([3, 0], [14, 2], 8, [3, 1, 2, 0], 0)
+    wide = np.full((2, 9), -9)
+    got = run_grow(*a, wide, 20, positions=False, width=4)
+    want = kv_ref.grow(*a, wide[:, :4], 20)
+    assert np.array_equal(got[0][:, :4], want[0]) and (got[0][:, 4:] == -9).all()
+    assert got[4] == want[4]
+
+
+@pytest.mark.parametrize("R", [1, 64, 700, 1024, 1500])
+@pytest.mark.parametrize("page", [1, 16, 100])
+def test_shrink(R, page):
+    rng = np.random.default_rng(R + page)
+    lengths, table, pool, used = batch(rng, R, page, 5 * page, 8)
+    keep = [int(rng.integers(0, n + 1)) if r % 3 else 0 for r, n in enumerate(lengths)]
+    check_shrink(lengths, keep, page, pool, used, table)
+
+
+def check_shrink(lengths, keep, page, free, cursor, table):
+    R = len(lengths)
+    pool, lo, co, st = dev(free), dev([7] * R), dev([7]), dev([7, 7])
+    t = dev(table)
+    lb.spmv_kv_shrink(dev(lengths), dev(keep), page, pool, dev([cursor]), t, lo, co, st)
+    got = (pool.tolist(), lo.tolist(), int(co), tuple(st.tolist()))
+    assert got == tuple(kv_ref.shrink(lengths, keep, page, free, cursor, table))
+    assert np.array_equal(t.cpu().numpy(), table)
+    return got
+
+
+@pytest.mark.parametrize("case,code", [
+    (dict(keep=[0, 18]), 2), (dict(keep=[-1, 0]), 2), (dict(lengths=[65, 17]), 2),
+    (dict(cursor=2), 1), (dict(cursor=-3), 1)])
+def test_shrink_is_all_or_nothing(case, code):
+    a = dict(lengths=[30, 17], keep=[1, 0], page=16, free=[9, 8, 7, 6], cursor=3,
+             table=np.arange(8).reshape(2, 4))
+    a.update(case)
+    assert check_shrink(*a.values())[-1][0] == code
+
+
+def test_a_chain_of_steps_returns_every_page():
+    """Requests come, grow, lose tokens and end; the pool ends as a permutation of what it
+    began with, and no page is ever held twice."""
+    rng = np.random.default_rng(9)
+    R, page, width, n_pages = 40, 8, 16, 400
+    pt = lb.PageTable(R, width, n_pages, page)
+    ref = dict(lengths=[0] * R, cursor=0, free=list(range(n_pages)),
+               table=np.full((R, width), -1, dtype=np.int64))
+    for step in range(30):
+        new = [int(rng.integers(0, min(20, width * page - n) + 1)) for n in ref["lengths"]]
+        n_tokens = sum(new) + 3
+        slots, pos = pt.grow(dev(new), n_tokens)
+        out = kv_ref.grow(ref["lengths"], new, page, ref["free"], ref["cursor"], ref["table"],
+                          n_tokens)
+        ref["table"], ref["lengths"], ref["cursor"] = out[0], out[1], out[2]
+        assert pt.status == out[6]
+        assert slots.tolist() == out[4] and pos.tolist() == out[5]
+        assert pt.lengths.tolist() == ref["lengths"] and int(pt.cursor) == ref["cursor"]
+        used = [int(slot) for slot in out[4] if slot >= 0]
+        assert len(set(used)) == len(used)
+        keep = [0 if rng.random() < 0.2 else n - min(n, int(rng.integers(0, 4)))
+                for n in ref["lengths"]]
+        pt.shrink(dev(keep))
+        ref["free"], ref["lengths"], ref["cursor"], st = kv_ref.shrink(
+            ref["lengths"], keep, page, ref["free"], ref["cursor"], ref["table"])
+        assert pt.status == st == (0, 0)
+        assert pt.free_pages.tolist() == ref["free"]
+    pt.shrink(dev([0] * R))
+    assert int(pt.cursor) == 0 and sorted(pt.free_pages.tolist()) == list(range(n_pages))
+
+
+def test_graph_replays_match_the_eager_calls():
+    """Two steps (one each way between the double buffers) captured and replayed."""
+    R, page = 50, 16
+    one = torch.ones(R, dtype=torch.int32, device="cuda")
+    pt, eager = lb.PageTable(R, 10, 500, page), lb.PageTable(R, 10, 500, page)
+    bufs = [torch.zeros(R, dtype=torch.int32, device="cuda") for _ in range(4)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            pt.grow(one, R, bufs[0], bufs[1])
+            pt.grow(one, R, bufs[2], bufs[3])
+    torch.cuda.current_stream().wait_stream(s)
+    for replay in range(20):
+        g.replay()
+        a = eager.grow(one, R)
+        b = eager.grow(one, R)
+        torch.cuda.synchronize()
+        for got, want in zip(bufs, a + b):
+            assert torch.equal(got, want), replay
+        assert torch.equal(pt.table, eager.table) and torch.equal(pt.lengths, eager.lengths)

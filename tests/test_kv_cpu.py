@@ -1,0 +1,195 @@
+"""The paged-cache operators' C ABI on the CPU: header and binding agree, and
+bad arguments are refused before any device call is made."""
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import load_balanced_csr_amd as lb
+from load_balanced_csr_amd import kv
+import kv_ref
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def test_header_and_binding_agree():
+    src = open(os.path.join(ROOT, "include", "spmv_kv.h")).read()
+    names = set(re.findall(r"SPMV_API\s+[\w\s\*]+?\b(spmv_\w+)\s*\(", src))
+    assert names == set(lb.KV_EXPORTED)
+    for name in names:
+        assert hasattr(lb.load(), name), name
+
+
+def test_struct_layout_matches_the_header(tmp_path):
+    cc = shutil.which("gcc")
+    if cc is None or not os.path.isdir("/opt/rocm/include"):
+        pytest.skip("no C compiler or ROCm headers")
+    fields = [f for f, _ in kv.KvCacheStruct._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "spmv_kv.h"\n'
+                   "int main(void) {\n"
+                   + "".join('printf("%%zu\\n", offsetof(spmv_kv_cache_t, %s));\n' % f
+                             for f in fields)
+                   + 'printf("%zu\\n", sizeof(spmv_kv_cache_t));\nreturn 0; }\n')
+    exe = tmp_path / "layout"
+    subprocess.check_call([cc, "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROOT, "include"), "-I",
+                           "/opt/rocm/include", str(src), "-o", str(exe)])
+    got = [int(x) for x in subprocess.check_output([str(exe)]).split()]
+    assert got == [getattr(kv.KvCacheStruct, f).offset for f in fields] + \
+        [ctypes.sizeof(kv.KvCacheStruct)]
+
+
+def _grow(**kw):
+    a = dict(n=4, lengths=0x10000, n_new=0x20000, page=16, free=0x30000, n_free=64,
+             cursor=0x40000, table=0x50000, stride=8, width=8, lengths_out=0x60000,
+             cursor_out=0x70000, token_ptr=0x80000, slots=0x90000, positions=0xa0000,
+             n_tokens=32, status=0xb0000)
+    a.update(kw)
+    return kv._load().spmv_kv_grow(*a.values(), None)
+
+
+def _shrink(**kw):
+    a = dict(n=4, lengths=0x10000, keep=0x20000, page=16, free=0x30000, n_free=64,
+             cursor=0x40000, table=0x50000, stride=8, width=8, lengths_out=0x60000,
+             cursor_out=0x70000, status=0xb0000)
+    a.update(kw)
+    return kv._load().spmv_kv_shrink(*a.values(), None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(n=-1), 1), (dict(page=0), 1), (dict(page=-4), 1), (dict(width=-1), 1),
+    (dict(n_free=-1), 1), (dict(stride=7), 1), (dict(lengths=None), 1), (dict(cursor=None), 1),
+    (dict(table=None), 1), (dict(status=None), 1), (dict(lengths_out=None), 1),
+    (dict(cursor_out=None), 1), (dict(free=None), 1),
+    (dict(lengths_out=0x10000), 1),            # in place: another workgroup may still read
+    (dict(cursor_out=0x40000), 1),
+    (dict(status=0x60004), 1),
+    (dict(width=2 ** 27, stride=2 ** 27), 2),  # width * page = 2^31
+    (dict(n_free=2 ** 31), 2), (dict(n=2 ** 31), 2)])
+def test_grow_and_shrink_refuse(bad, status):
+    assert _grow(**bad) == status, lb.spmv_last_error()
+    assert _shrink(**bad) == status, lb.spmv_last_error()
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(n_tokens=-1), 1), (dict(n_new=None), 1), (dict(token_ptr=None), 1),
+    (dict(slots=None), 1), (dict(token_ptr=0x90000), 1), (dict(positions=0x90004), 1),
+    (dict(table=0x30000), 1), (dict(n_tokens=2 ** 31), 2)])
+def test_grow_refuses(bad, status):
+    assert _grow(**bad) == status, lb.spmv_last_error()
+
+
+def test_shrink_refuses():
+    assert _shrink(keep=None) == 1
+    assert _shrink(free=0x50000) == 1          # the pool over the table
+
+
+def _cache(**kw):
+    a = dict(k=0x1000000, v=0x2000000, k_scale=None, v_scale=None, n_pages=10, k_page=8192,
+             k_token=512, k_head=128, v_page=8192, v_token=512, v_head=128, page_size=16,
+             n_heads=4, head_dim=128, dtype=kv.KV_BF16)
+    a.update(kw)
+    return kv.KvCacheStruct(*a.values())
+
+
+BAD_CACHES = [
+    (dict(k=None), 1), (dict(v=None), 1), (dict(n_pages=0), 1), (dict(page_size=0), 1),
+    (dict(n_heads=0), 1), (dict(head_dim=0), 1), (dict(head_dim=264), 2), (dict(head_dim=100), 1),
+    (dict(dtype=9), 1), (dict(dtype=-1), 1), (dict(k=0x1000008), 1), (dict(v_token=516), 1),
+    (dict(k_head=-128), 1), (dict(n_pages=2 ** 27), 2), (dict(k_scale=0x5000), 1),
+    (dict(dtype=kv.KV_F8E4M3, head_dim=72), 1)]
+
+
+def _append(cache, **kw):
+    a = dict(n=3, k=0x3000000, k0=512, k1=128, v=0x4000000, v0=512, v1=128, dtype=kv.KV_BF16,
+             slots=0x5000000)
+    a.update(kw)
+    return kv._load().spmv_kv_append(ctypes.addressof(cache), *a.values(), None)
+
+
+def _attend(cache, **kw):
+    a = dict(n=3, heads=8, q=0x3000000, q0=1024, q1=128, dtype=kv.KV_BF16, table=0x5000000,
+             stride=4, width=4, lengths=0x6000000, scale=1.0, window=0, sinks=0, out=0x4000000,
+             o0=1024, o1=128, lse=None, ws=0x40000000, wb=1 << 30)
+    a.update(kw)
+    return kv._load().spmv_kv_attention(ctypes.addressof(cache), *a.values(), None)
+
+
+@pytest.mark.parametrize("bad,status", BAD_CACHES)
+def test_bad_caches_are_refused(bad, status):
+    n = ctypes.c_size_t(0)
+    cache = _cache(**bad)
+    assert _append(cache) == status, lb.spmv_last_error()
+    assert _attend(cache) == status, lb.spmv_last_error()
+    assert kv._load().spmv_kv_attention_workspace_size(
+        ctypes.addressof(cache), 8, ctypes.addressof(n)) == status
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(n=-1), 1), (dict(dtype=kv.KV_F16), 1), (dict(dtype=kv.KV_F8E4M3), 1), (dict(dtype=7), 1),
+    (dict(k=None), 1), (dict(v=None), 1), (dict(slots=None), 1), (dict(k=0x3000001), 1),
+    (dict(k0=-1), 1), (dict(v1=-1), 1), (dict(k=0x1000100), 1), (dict(v=0x2000000), 1),
+    (dict(n=2 ** 31), 2)])
+def test_append_refuses(bad, status):
+    assert _append(_cache(), **bad) == status, lb.spmv_last_error()
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(n=-1), 1), (dict(heads=0), 1), (dict(heads=6), 1), (dict(dtype=kv.KV_F32), 1),
+    (dict(dtype=kv.KV_F8E4M3), 1), (dict(q=None), 1), (dict(out=None), 1), (dict(lengths=None), 1),
+    (dict(table=None), 1), (dict(stride=3), 1), (dict(window=-1), 1), (dict(sinks=-2), 1),
+    (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(out=0x3000000), 1),
+    (dict(lse=0x4000000), 1), (dict(q0=-1), 1), (dict(o1=64), 1), (dict(o0=0), 1),
+    (dict(q=0x3000001), 1), (dict(out=0x1000000), 1), (dict(width=2 ** 27, stride=2 ** 27), 2),
+    (dict(n=2 ** 28), 2), (dict(ws=0x40000008), 1)])
+def test_attention_refuses(bad, status):
+    assert _attend(_cache(), **bad) == status, lb.spmv_last_error()
+
+
+def test_attention_refuses_32_bit_queries_of_an_8_bit_cache_and_a_short_workspace():
+    c = _cache(dtype=kv.KV_F8E4M3)
+    assert _attend(c, dtype=kv.KV_F32) == 1
+    n = ctypes.c_size_t(0)
+    assert kv._load().spmv_kv_attention_workspace_size(ctypes.addressof(c), 8, None) == 1
+    assert kv._load().spmv_kv_attention_workspace_size(ctypes.addressof(c), 7,
+                                                       ctypes.addressof(n)) == 1
+    assert kv._load().spmv_kv_attention_workspace_size(ctypes.addressof(c), 8,
+                                                       ctypes.addressof(n)) == 0
+    if n.value:
+        assert _attend(c, wb=n.value - 1) == 1
+        assert _attend(c, ws=None) == 1
+
+
+def test_nothing_to_do_needs_no_device():
+    assert _append(_cache(), n=0) == 0
+    assert _attend(_cache(), n=0) == 0
+
+
+def test_binding_refuses_host_tensors_and_wrong_types():
+    i = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="device"):
+        lb.KvCache(torch.zeros(2, 4, 1, 64), torch.zeros(2, 4, 1, 64))
+    with pytest.raises(TypeError, match="dtype"):
+        lb.KvCache(torch.zeros(2, 4, 1, 64, dtype=torch.float64), torch.zeros(2, 4, 1, 64))
+    with pytest.raises(ValueError, match="device"):
+        lb.spmv_kv_grow(i, i, 16, i, i, i.view(2, 2), i, i, i, i, None, i)
+    with pytest.raises(TypeError, match="int32"):
+        lb.spmv_kv_shrink(i, i, 16, i, i, i.long().view(2, 2), i, i, i)
+
+
+def test_the_8_bit_reference_against_torch():
+    g = torch.Generator().manual_seed(3)
+    x = torch.cat([torch.randn(4000, generator=g) * 100, torch.randn(4000, generator=g) * 1e-2,
+                   torch.tensor([0.0, -0.0, 448.0, 447.0, 432.0, 440.0, 2.0 ** -9, 2.0 ** -10,
+                                 3 * 2.0 ** -10, float("nan")])]).clamp(-448, 448)
+    want = x.to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    got = kv_ref.to_e4m3(x.numpy())
+    nan = np.isnan(x.numpy())
+    assert np.array_equal(got[~nan], want[~nan]) and np.all(got[nan] & 0x7f == 0x7f)
+    assert np.array_equal(kv_ref.to_e4m3(np.float32([500, -500, np.inf, -np.inf])),
+                          np.uint8([0x7e, 0xfe, 0x7e, 0xfe]))
