@@ -99,8 +99,8 @@ typedef struct spmv_kv_cache {
  * counts as both: entries below held[r] are read, those above are written;
  * lengths_out and cursor_out are arrays of their own, so that a step can be
  * run again). SPMV_ERR_INVALID_ARG for NULL or overlapping arrays or a
- * negative size; SPMV_ERR_UNSUPPORTED when table_width * page_size, n_free,
- * n_requests or n_tokens passes 2^31 - 1. One launch. */
+ * negative size; SPMV_ERR_UNSUPPORTED when table_width * page_size passes
+ * 2^31 - 65 or n_free, n_requests or n_tokens 2^31 - 1. One launch. */
 SPMV_API spmv_status_t spmv_kv_grow(int64_t n_requests, const int32_t* lengths,
                                     const int32_t* n_new, int32_t page_size,
                                     const int32_t* free_pages, int64_t n_free,
@@ -155,7 +155,8 @@ SPMV_API spmv_status_t spmv_kv_append(const spmv_kv_cache_t* cache, int64_t n_to
  *   out[r][h][:] = sum_t exp(s[t] - m) v[t][:] / sum_t exp(s[t] - m), m = max s
  *   lse[r][h] = m + log(sum_t exp(s[t] - m))
  *
- * A row with no visible token (length 0) gives out = 0 and lse = -inf. A
+ * A row with no visible token (length 0), or none whose score is above -inf,
+ * gives out = 0 and lse = -inf. A
  * length below 0 counts as 0, one beyond table_width * page_size as that; a
  * token on a page outside [0, n_pages) is not visible. Slots that hold no
  * visible token are never part of a result, whatever they hold; NaN and
@@ -173,8 +174,8 @@ SPMV_API spmv_status_t spmv_kv_append(const spmv_kv_cache_t* cache, int64_t n_to
  * need one each. The size does not depend on n_requests or lengths.
  * SPMV_ERR_INVALID_ARG for a bad cache, size, type, overlap, a negative
  * window or sinks, a scale that is not finite or a short workspace;
- * SPMV_ERR_UNSUPPORTED when table_width * page_size or n_requests * n_q_heads
- * passes 2^31 - 1. */
+ * SPMV_ERR_UNSUPPORTED when table_width * page_size passes 2^31 - 65 or
+ * n_requests * n_q_heads 2^31 - 1. */
 SPMV_API spmv_status_t spmv_kv_attention_workspace_size(const spmv_kv_cache_t* cache,
                                                         int32_t n_q_heads, size_t* bytes);
 SPMV_API spmv_status_t spmv_kv_attention(const spmv_kv_cache_t* cache, int64_t n_requests,

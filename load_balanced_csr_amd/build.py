@@ -17,7 +17,8 @@ SOURCES = ["api.hip", "plan_kernels.hip", "merge_kernels.hip", "binned_kernels.h
            "group_kernels.hip", "noalloc.hip",
            "tile_kernels.hip", "slab_kernels.hip",
            "kv_api.hip", "kv_table_kernels.hip", "kv_append_kernels.hip",
-           "kv_attention_kernels.hip"]
+           "kv_attention_kernels.hip", "kv_attention_f32.hip", "kv_attention_f16.hip",
+           "kv_attention_bf16.hip", "kv_attention_f8_f16.hip", "kv_attention_f8_bf16.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

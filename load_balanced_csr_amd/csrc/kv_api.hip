@@ -127,7 +127,9 @@ spmv_status_t check_table(int64_t n_requests, int32_t page_size, const void* tab
   if (n_requests > 1 && table_stride < table_width)
     return fail(SPMV_ERR_INVALID_ARG, "table_stride %lld < table_width %lld",
                 (long long)table_stride, (long long)table_width);
-  if (n_requests > kInt32Max || table_width > kInt32Max / page_size)
+  // 64 below the end of int32: the attention numbers the tokens of a whole
+  // step, past a row's last one
+  if (n_requests > kInt32Max || table_width > (kInt32Max - 64) / page_size)
     return fail(SPMV_ERR_UNSUPPORTED, "n_requests or table_width * page_size beyond int32");
   if (n_requests > 0 && table_width > 0 && !table)
     return fail(SPMV_ERR_INVALID_ARG, "table is NULL");
@@ -301,7 +303,7 @@ spmv_status_t spmv_kv_attention_workspace_size(const spmv_kv_cache_t* cache, int
                                                size_t* bytes) {
   if (!bytes) return fail(SPMV_ERR_INVALID_ARG, "bytes is NULL");
   if (spmv_status_t st = check_heads(cache, n_q_heads)) return st;
-  *bytes = kv_attention_workspace(cache->n_heads, n_q_heads / cache->n_heads, cache->head_dim);
+  *bytes = kv_attention_workspace(n_q_heads / cache->n_heads, cache->head_dim, cache->dtype);
   return SPMV_SUCCESS;
 }
 
@@ -333,7 +335,7 @@ spmv_status_t spmv_kv_attention(const spmv_kv_cache_t* cache, int64_t n_requests
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) % eb)
     return fail(SPMV_ERR_INVALID_ARG, "q and out must be aligned to their elements");
   const int group = n_q_heads / cache->n_heads;
-  const size_t need = kv_attention_workspace(cache->n_heads, group, cache->head_dim);
+  const size_t need = kv_attention_workspace(group, cache->head_dim, cache->dtype);
   if (workspace_bytes < need || (need && !workspace))
     return fail(SPMV_ERR_INVALID_ARG, "workspace of %zu bytes needed, %zu given", need,
                 workspace ? workspace_bytes : 0);
@@ -390,6 +392,13 @@ spmv_status_t spmv_kv_attention(const spmv_kv_cache_t* cache, int64_t n_requests
   a.sinks = (int32_t)(sinks < kInt32Max ? sinks : kInt32Max);
   a.cache_dtype = cache->dtype;
   a.dtype = dtype;
+  a.min_share = 4;
+  a.n_cus = 256;
+  a.q_aligned = !((reinterpret_cast<uintptr_t>(q) |
+                   (uintptr_t)((q_request_stride | q_head_stride) * eb)) & 15);
+  a.out_aligned = !((reinterpret_cast<uintptr_t>(out) |
+                     (uintptr_t)((out_request_stride | out_head_stride) * eb)) &
+                    (uintptr_t)(4 * eb - 1));
   a.scale = (float)scale;
   a.page = make_fastdiv((uint32_t)cache->page_size);
   return launched(launch_kv_attention(a, stream), "spmv_kv_attention launch");

@@ -79,10 +79,18 @@ struct KvAttentionArgs {
   int32_t n_requests, n_kv_heads, group, head_dim;   // group: query heads per key head
   int32_t window, sinks;       // window 0: all tokens
   int32_t cache_dtype, dtype;
+  int32_t min_share;           // least units (tiles and rows) of one workgroup
+  int32_t n_cus;
+  bool q_aligned, out_aligned; // 16-byte loads of q, four-element stores of out
   float scale;
   FastDiv page;
 };
 hipError_t launch_kv_attention(const KvAttentionArgs& a, hipStream_t s);
-size_t kv_attention_workspace(int n_kv_heads, int group, int head_dim);
+size_t kv_attention_workspace(int group, int head_dim, int cache_dtype);
+hipError_t launch_kv_attention_f32(const KvAttentionArgs& a, hipStream_t s);
+hipError_t launch_kv_attention_f16(const KvAttentionArgs& a, hipStream_t s);
+hipError_t launch_kv_attention_bf16(const KvAttentionArgs& a, hipStream_t s);
+hipError_t launch_kv_attention_f8_f16(const KvAttentionArgs& a, hipStream_t s);
+hipError_t launch_kv_attention_f8_bf16(const KvAttentionArgs& a, hipStream_t s);
 
 }  // namespace spmv
