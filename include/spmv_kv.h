@@ -175,7 +175,7 @@ SPMV_API spmv_status_t spmv_kv_append(const spmv_kv_cache_t* cache, int64_t n_to
  * SPMV_ERR_INVALID_ARG for a bad cache, size, type, overlap, a negative
  * window or sinks, a scale that is not finite or a short workspace;
  * SPMV_ERR_UNSUPPORTED when table_width * page_size passes 2^31 - 65 or
- * n_requests * n_q_heads 2^31 - 1. */
+ * n_requests * n_q_heads 2^28. */
 SPMV_API spmv_status_t spmv_kv_attention_workspace_size(const spmv_kv_cache_t* cache,
                                                         int32_t n_q_heads, size_t* bytes);
 SPMV_API spmv_status_t spmv_kv_attention(const spmv_kv_cache_t* cache, int64_t n_requests,

@@ -328,8 +328,8 @@ spmv_status_t spmv_kv_attention(const spmv_kv_cache_t* cache, int64_t n_requests
     return fail(SPMV_ERR_INVALID_ARG, "negative stride");
   if (window < 0 || sinks < 0) return fail(SPMV_ERR_INVALID_ARG, "window or sinks below 0");
   if (!std::isfinite(scale)) return fail(SPMV_ERR_INVALID_ARG, "scale is not finite");
-  if (n_requests > kInt32Max / n_q_heads)
-    return fail(SPMV_ERR_UNSUPPORTED, "n_requests * n_q_heads beyond int32");
+  if (n_requests > (int64_t(1) << 28) / n_q_heads)
+    return fail(SPMV_ERR_UNSUPPORTED, "n_requests * n_q_heads beyond 2^28");
   if (n_requests == 0) return SPMV_SUCCESS;
   if (!q || !out || !lengths) return fail(SPMV_ERR_INVALID_ARG, "NULL array");
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) % eb)
@@ -392,8 +392,6 @@ spmv_status_t spmv_kv_attention(const spmv_kv_cache_t* cache, int64_t n_requests
   a.sinks = (int32_t)(sinks < kInt32Max ? sinks : kInt32Max);
   a.cache_dtype = cache->dtype;
   a.dtype = dtype;
-  a.min_share = 4;
-  a.n_cus = 256;
   a.q_aligned = !((reinterpret_cast<uintptr_t>(q) |
                    (uintptr_t)((q_request_stride | q_head_stride) * eb)) & 15);
   a.out_aligned = !((reinterpret_cast<uintptr_t>(out) |

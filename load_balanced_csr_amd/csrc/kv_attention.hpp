@@ -38,6 +38,9 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "kv_internal.hpp"
 #include "kv_types.hpp"
@@ -49,8 +52,12 @@ typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef f16 f16x2 __attribute__((ext_vector_type(2)));
 
-// Rows that a partial slot holds, and workgroups the workspace is laid out for.
-constexpr int kKvMaxBlocks = 1024;
+constexpr int kKvWaves = 4;              // wavefronts of one workgroup
+constexpr int kKvBlock = kKvWaves * kWave;
+
+constexpr int kKvCus = 256;
+// Workgroups the workspace is laid out for: two slots and four counters each.
+constexpr int kKvMaxBlocks = 2 * kKvCus;
 
 constexpr int kv_dim_pad(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 // 16-row blocks of query heads one workgroup takes: two when a key head has
@@ -60,9 +67,24 @@ constexpr int kv_row_blocks(int group, int cache_dtype) {
   return group > 16 && cache_dtype != SPMV_KV_F32 ? 2 : 1;
 }
 constexpr size_t kv_slot_floats(int nb, int dpad) { return (size_t)16 * nb * (dpad + 2); }
-constexpr size_t kKvCounterBytes = kKvMaxBlocks * sizeof(int32_t);
+// two counters for each slot: arrivals at a group of parts, and of groups at a row
+constexpr size_t kKvCounterBytes = 4 * kKvMaxBlocks * sizeof(int32_t);
+constexpr int kKvFlatJoin = 16;
+// Units (steps and row costs) of the shortest run one workgroup takes.
+constexpr int kKvMinRun = 4;
 
 #if defined(__HIP_DEVICE_COMPILE__)
+
+// A value that is the same in all lanes, in scalar registers. What comes out
+// of LDS or a vector load is not known to be so, and one such value in a row's
+// coordinates would put its addresses and branches into vector registers.
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+// p[i] for uniform p and i, by a scalar load: counted apart from the vector
+// loads, so waiting for it does not wait for keys and values in flight.
+__device__ __forceinline__ int32_t scalar_load(const int32_t* p, int64_t i) {
+  return reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(
+      reinterpret_cast<uint64_t>(p))[i];
+}
 
 // Maximum and sum over the four lanes that share a query column (c, c + 16,
 // c + 32, c + 48).
@@ -120,6 +142,36 @@ __device__ __forceinline__ void split2(float p0, float p1, f16, uint32_t& hi, ui
   lo = __builtin_bit_cast(uint32_t, r);
 }
 
+// Parts of a row pass between workgroups of different XCDs, whose L2 caches
+// are apart: device-scope stores that write through and loads that do not take
+// a stale line. (Fences at device scope would write back and drop a whole L2
+// each time.)
+__device__ __forceinline__ void share(float* p, float x) {
+  __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void share4(float* p, f32x4 x) {
+  uint64_t* q = reinterpret_cast<uint64_t*>(p);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    __hip_atomic_store(q + h, (uint64_t)__float_as_uint(x[2 * h]) |
+                                  (uint64_t)__float_as_uint(x[2 * h + 1]) << 32,
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float shared(const float* p) {
+  return __hip_atomic_load(const_cast<float*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x4 shared4(const float* p) {
+  uint64_t* q = reinterpret_cast<uint64_t*>(const_cast<float*>(p));
+  f32x4 x;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint64_t y = __hip_atomic_load(q + h, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    x[2 * h] = __uint_as_float((uint32_t)y);
+    x[2 * h + 1] = __uint_as_float((uint32_t)(y >> 32));
+  }
+  return x;
+}
+
 #endif  // __HIP_DEVICE_COMPILE__
 
 // What one instantiation works with. C: cache, Q: queries and output.
@@ -152,9 +204,9 @@ struct KvSpan {
   int32_t s0, s1, steps;     // step i of the row is i < s0 ? i : s1 + i - s0
 };
 template <int ST>
-__device__ __forceinline__ KvSpan kv_span(const KvAttentionArgs& a, int r) {
+__device__ __forceinline__ KvSpan kv_span(const KvAttentionArgs& a, int32_t length) {
   KvSpan x;
-  x.n = min(max(a.lengths[r], 0), a.table_tokens);
+  x.n = min(max(length, 0), a.table_tokens);
   x.from = a.window && x.n > a.window ? x.n - a.window : 0;
   x.first = min(a.sinks, x.from);
   x.s0 = (int32_t)(((uint32_t)x.first + ST - 1) / ST);
@@ -162,58 +214,200 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttentionArgs& a, int r) {
   x.steps = x.s0 + (int32_t)(((uint32_t)x.n + ST - 1) / ST) - x.s1;
   return x;
 }
-__device__ __forceinline__ int32_t kv_tiles(const KvSpan& x) {
-  return (x.steps + kWavesPerBlock - 1) / kWavesPerBlock;
+// What a row costs, in units of one step (of 1 << step_shift steps where the
+// host has found that the rows' costs could pass 30 bits otherwise): its steps
+// and kKvRowCost for beginning and ending it, or one for a row without any.
+constexpr int32_t kKvRowCost = 4;
+__device__ __forceinline__ int32_t kv_units(const KvAttentionArgs& a, const KvSpan& x) {
+  return (int32_t)(((uint32_t)x.steps + (1u << a.step_shift) - 1) >> a.step_shift);
+}
+__device__ __forceinline__ int32_t kv_cost(int32_t units) {
+  return units > 0 ? units + kKvRowCost : 1;
 }
 
-// One workgroup's part of a row ready to be written or joined: m, l per row
-// in LDS, o of each wavefront in LDS, scaled to the common maximum.
+// The rows' units cut into runs, one for each workgroup, whose lengths differ
+// by one at most; none shorter than kKvMinRun, however few rows there are.
+struct KvShares {
+  int32_t runs, base, longer;      // runs of base + 1 units, then of base
+};
+__device__ __forceinline__ KvShares kv_shares(int32_t total, uint32_t most) {
+  const int32_t runs = min((int32_t)most, max(total / kKvMinRun, 1));
+  return KvShares{runs, (int32_t)((uint32_t)total / (uint32_t)runs),
+                  (int32_t)((uint32_t)total % (uint32_t)runs)};
+}
+__device__ __forceinline__ int32_t kv_begin(const KvShares& s, int32_t w) {
+  return w * s.base + min(w, s.longer);
+}
+__device__ __forceinline__ int32_t kv_owner(const KvShares& s, int32_t unit) {
+  const int32_t cut = s.longer * (s.base + 1);
+  return unit < cut ? (uint32_t)unit / (uint32_t)(s.base + 1)
+                    : s.longer + (uint32_t)(unit - cut) / (uint32_t)s.base;
+}
+
+// A row (request r, key head and block of query heads hc) that more than one
+// workgroup takes, and the unit of its first step.
+struct KvCut {
+  int32_t r, hc, steps_at, units;
+};
+
+// How a cut row's parts come together. They are those of workgroups b0 .. b1,
+// in slot 2 b + 1 for the one that begins it and 2 b for those that go on with
+// it (a workgroup begins and goes on with one row at most). Up to kKvFlatJoin
+// parts are joined at once, more in two levels of about sqrt(parts): groups of
+// consecutive parts, then the groups.
+struct KvJoin {
+  int32_t b0, b1, per_group, groups;
+  __device__ __forceinline__ int32_t slot(int32_t b) const { return 2 * b + (b == b0 ? 1 : 0); }
+  __device__ __forceinline__ int32_t group(int32_t b) const {
+    return (uint32_t)(b - b0) / (uint32_t)per_group;
+  }
+  __device__ __forceinline__ int32_t counter(int32_t b) const {
+    return slot(b0 + group(b) * per_group);
+  }
+  __device__ __forceinline__ int32_t in_group(int32_t b) const {
+    return min(per_group, b1 - b0 + 1 - group(b) * per_group);
+  }
+};
+__device__ __forceinline__ KvJoin kv_join_of(const KvShares& s, const KvCut& c) {
+  KvJoin j{0, 0, 1, 1};
+  if (c.r < 0) return j;
+  j.b0 = kv_owner(s, c.steps_at);
+  j.b1 = kv_owner(s, c.steps_at + c.units - 1);
+  const int32_t parts = j.b1 - j.b0 + 1;
+#if defined(__HIP_DEVICE_COMPILE__)
+  j.per_group = parts <= kKvFlatJoin
+                    ? parts
+                    : uniform((int32_t)ceilf(__builtin_amdgcn_sqrtf((float)parts)));
+#endif
+  j.groups = (int32_t)((uint32_t)(parts + j.per_group - 1) / (uint32_t)j.per_group);
+  return j;
+}
+
+// Four elements of a row of a part, with the row's maximum and sum.
+struct KvPart {
+  float m, l;
+  f32x4 o;
+};
+
+#if defined(__HIP_DEVICE_COMPILE__)
+
+// Whether this is the last of `many` arrivals at the counter, which is then 0
+// again for the next call.
+__device__ __forceinline__ bool arrive(int32_t* counter, int32_t many) {
+  const bool last = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT) == many - 1;
+  if (last) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return last;
+}
+
+// The join of `many` parts b, b + by, .. in that order.
+template <int ROWS, int DPAD>
+__device__ __forceinline__ KvPart kv_join(const float* slots, const KvJoin& j, int32_t b,
+                                          int32_t by, int32_t many, int row, int d) {
+  constexpr int64_t SLOT = (int64_t)kv_slot_floats(ROWS / 16, DPAD);
+  constexpr int AT_ONCE = 8;                     // parts whose loads are in flight together
+  KvPart p{-INFINITY, 0.f, f32x4{0.f, 0.f, 0.f, 0.f}};
+  for (int32_t i0 = 0; i0 < many; i0 += AT_ONCE) {
+    float pm[AT_ONCE], pl[AT_ONCE];
+    f32x4 po[AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const float* s = slots + j.slot(b + min(i0 + i, many - 1) * by) * SLOT;
+      pm[i] = shared(s + row);
+      pl[i] = shared(s + ROWS + row);
+      po[i] = shared4(s + 2 * ROWS + row * DPAD + d);
+    }
+    float now = p.m;
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i)
+      if (i0 + i < many) now = fmaxf(now, pm[i]);
+    const float base = now == -INFINITY ? 0.f : now;
+    const float keep = __builtin_amdgcn_exp2f(p.m - base);
+    p.m = now;
+    p.l *= keep;
+    p.o *= keep;
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      if (i0 + i < many) {
+        const float w = __builtin_amdgcn_exp2f(pm[i] - base);
+        p.l += pl[i] * w;
+        p.o += po[i] * w;
+      }
+    }
+  }
+  return p;
+}
+
+// out and lse of four elements of a row: o / l, or 0 where nothing was summed.
+template <typename Q>
+__device__ __forceinline__ void kv_write(const KvAttentionArgs& a, int r, int64_t q_head, int d,
+                                         f32x4 o, float m, float l, float vscale) {
+  Q* out = static_cast<Q*>(a.out) + r * a.out_request + q_head * a.out_head + d;
+  const float inv = vscale / l;
+  alignas(16) Q y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = from_f32<Q>(l == 0.f ? 0.f : o[e] * inv);
+  if (a.out_aligned) {
+    if constexpr (sizeof(Q) == 4)
+      *reinterpret_cast<u32x4*>(out) = *reinterpret_cast<const u32x4*>(y);
+    else
+      *reinterpret_cast<u32x2*>(out) = *reinterpret_cast<const u32x2*>(y);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[e] = y[e];
+  }
+  if (a.lse && d == 0)
+    a.lse[(int64_t)r * a.n_kv_heads * a.group + q_head] =
+        l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.693147180559945f;
+}
+
+#endif  // __HIP_DEVICE_COMPILE__
+
 template <typename C, typename Q, int DPAD, int NB, bool EXACT, bool PAGED16, int OCC>
-__global__ __launch_bounds__(kBlock, OCC) void kv_attention_kernel(KvAttentionArgs a) {
+__global__ __launch_bounds__(kKvBlock, OCC) void kv_attention_kernel(KvAttentionArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef KvShape<C, Q, DPAD, NB> S;
   constexpr int ST = S::ST, TS = S::TS, ROWS = 16 * NB, PITCH = DPAD + 4;
-  __shared__ __align__(16) float red[kWavesPerBlock][ROWS][PITCH];
-  __shared__ float wave_m[kWavesPerBlock][ROWS], wave_l[kWavesPerBlock][ROWS];
-  __shared__ int64_t scan[kWavesPerBlock];
-  __shared__ int64_t found_before;
-  __shared__ int32_t found_row, last_one;
+  __shared__ __align__(16) float red[kKvWaves][ROWS][PITCH];
+  __shared__ float wave_m[kKvWaves][ROWS], wave_l[kKvWaves][ROWS];
+  __shared__ int32_t scan[kKvWaves];
+  __shared__ int32_t found_row, found_before, last_one[3];
 
   const int tid = threadIdx.x, lane = lane_id(), c = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int wave = uniform(tid / kWave);
   const int D = a.head_dim;
   const int chunks = (a.group + ROWS - 1) / ROWS;
   const int heads = a.n_kv_heads * chunks;       // rows per request
 
   // ---- this workgroup's run of the rows' costs -------------------------------
-  const int per_thread = (a.n_requests + kBlock - 1) / kBlock;
+  const int per_thread = (a.n_requests + kKvBlock - 1) / kKvBlock;
   const int r0 = min(tid * per_thread, a.n_requests);
   const int r1 = min(r0 + per_thread, a.n_requests);
-  int64_t mine = 0;
-  for (int r = r0; r < r1; ++r) mine += (int64_t)(kv_tiles(kv_span<ST>(a, r)) + 1) * heads;
-  int64_t incl = mine;
+  int32_t mine = 0;
+  for (int r = r0; r < r1; ++r)
+    mine += kv_cost(kv_units(a, kv_span<ST>(a, a.lengths[r]))) * heads;
+  int32_t incl = mine;
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
-    const int64_t x = __shfl_up(incl, d);
+    const int32_t x = __shfl_up(incl, d);
     if (lane >= d) incl += x;
   }
   if (lane == kWave - 1) scan[wave] = incl;
   __syncthreads();
-  int64_t before = incl - mine, total = 0;
+  int32_t before = incl - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w < kWavesPerBlock; ++w) {
+  for (int w = 0; w < kKvWaves; ++w) {
     if (w < wave) before += scan[w];
     total += scan[w];
   }
-  int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  per = per < a.min_share ? a.min_share : per;
-  const int64_t d0 = (int64_t)blockIdx.x * per;
-  if (d0 >= total) return;                       // the whole workgroup
-  const int64_t d1 = d0 + per < total ? d0 + per : total;
+  total = uniform(total);
+  const KvShares shares = kv_shares(total, gridDim.x);
+  if ((int32_t)blockIdx.x >= shares.runs) return;   // the whole workgroup
+  const int32_t d0 = kv_begin(shares, blockIdx.x), d1 = kv_begin(shares, blockIdx.x + 1);
   if (before <= d0 && d0 < before + mine) {
     int r = r0;
     for (;; ++r) {
-      const int64_t cost = (int64_t)(kv_tiles(kv_span<ST>(a, r)) + 1) * heads;
+      const int32_t cost = kv_cost(kv_units(a, kv_span<ST>(a, a.lengths[r]))) * heads;
       if (d0 < before + cost) break;
       before += cost;
     }
@@ -221,54 +415,65 @@ __global__ __launch_bounds__(kBlock, OCC) void kv_attention_kernel(KvAttentionAr
     found_before = before;
   }
   __syncthreads();
-  int r = __builtin_amdgcn_readfirstlane(found_row);
-  int64_t request_at = found_before;             // unit at which request r begins
+  int row_r = found_row;
+  int32_t row_before = found_before;             // unit at which request row_r begins
 
+  float* slots = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kKvCounterBytes);
+  constexpr int64_t SLOT = (int64_t)kv_slot_floats(NB, DPAD);
   const float sc = a.scale * 1.44269504088896f;
-  const int64_t k_token_b = a.k_token * (int64_t)sizeof(C), v_token_b = a.v_token * (int64_t)sizeof(C);
+  const int64_t k_token_b = a.k_token * (int64_t)sizeof(C);
+  const int64_t v_token_b = a.v_token * (int64_t)sizeof(C);
 
-  for (;; ++r) {
-    const KvSpan x = kv_span<ST>(a, r);
-    const int32_t tiles = kv_tiles(x), cost = tiles + 1;
-    int hc = d0 > request_at ? (int)((d0 - request_at) / cost) : 0;
-    for (; hc < heads; ++hc) {
-      // ---- the part of row (r, hc) in this run: tiles [ta, tb) ---------------
-      const int64_t row_at = request_at + (int64_t)hc * cost;
-      if (row_at >= d1) return;
-      const int32_t ta = d0 > row_at ? (int32_t)(d0 - row_at) - 1 : 0;
-      const int32_t tb = row_at + cost <= d1 ? tiles : (int32_t)(d1 - row_at) - 1;
-      const int32_t ta0 = ta < 0 ? 0 : ta;
-      if (tiles > 0 && tb <= ta0) continue;      // only the row's own unit: nothing to sum
-      const bool whole = ta0 == 0 && tb == tiles;
+  // rows cut at this run's two ends: their numbers and units (-1: none)
+  KvCut head_cut{-1, 0, 0, 0}, tail_cut{-1, 0, 0, 0};
+  for (bool more_rows = true; more_rows; ++row_r) {
+    const int r = uniform(row_r);
+    const int32_t request_at = uniform(row_before);
+    const KvSpan x = kv_span<ST>(a, scalar_load(a.lengths, r));
+    const int32_t units = kv_units(a, x), cost = kv_cost(units);
+    int hc0 = d0 > request_at ? (uint32_t)(d0 - request_at) / (uint32_t)cost : 0;
+    for (; hc0 < heads; ++hc0) {
+      const int hc = uniform(hc0);
+      // ---- the part of row (r, hc) in this run: its units [ua, ub) --------------
+      const int32_t row_at = request_at + hc * cost;
+      if (row_at >= d1) break;
+      const int32_t steps_at = row_at + cost - units;    // unit of its first step
+      const int32_t ua = max(d0 - steps_at, 0), ub = min(d1 - steps_at, units);
+      if (units > 0 ? ub <= ua : row_at < d0) continue;  // only what the row costs besides
+      const bool whole = ua == 0 && ub == units;
       const int kh = hc / chunks, first_head = (hc - kh * chunks) * ROWS;
       const int rows = min(ROWS, a.group - first_head);
       const int64_t q_head0 = (int64_t)kh * a.group + first_head;
 
       // ---- queries: B operands, zero past the group's last head ---------------
       uint32_t qf[NB][S::QW];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int row = nb * 16 + c;
-        const Q* qp = static_cast<const Q*>(a.q) + r * a.q_request + (q_head0 + row) * a.q_head;
+      auto load_q = [&](auto aligned) {
         constexpr int W = 4;                     // words per load: 16 bytes of queries
         constexpr int E = 16 / sizeof(Q);
 #pragma unroll
-        for (int i = 0; i < S::QW / W; ++i) {
-          // the elements that go with the i-th operand of a key
-          const int d = S::F8 ? (i / 2) * 64 + g * 16 + (i & 1) * 8 : i * 4 * E + g * E;
-          alignas(16) Q e[E] = {};
-          if (row < rows && d < D) {
-            if (a.q_aligned) {
-              *reinterpret_cast<u32x4*>(e) = *reinterpret_cast<const u32x4*>(qp + d);
-            } else {
+        for (int nb = 0; nb < NB; ++nb) {
+          const int row = nb * 16 + c;
+          const Q* qp = static_cast<const Q*>(a.q) + r * a.q_request + (q_head0 + row) * a.q_head;
 #pragma unroll
-              for (int j = 0; j < E; ++j) e[j] = qp[d + j];
+          for (int i = 0; i < S::QW / W; ++i) {
+            // the elements that go with the i-th operand of a key
+            const int d = S::F8 ? (i / 2) * 64 + g * 16 + (i & 1) * 8 : i * 4 * E + g * E;
+            u32x4 v = {0, 0, 0, 0};
+            if (row < rows && (EXACT || d < D)) {
+              if constexpr (decltype(aligned)::value) {
+                v = *reinterpret_cast<const u32x4*>(qp + d);
+              } else {
+                alignas(16) Q e[E];
+#pragma unroll
+                for (int j = 0; j < E; ++j) e[j] = qp[d + j];
+                v = *reinterpret_cast<const u32x4*>(e);
+              }
             }
-          }
 #pragma unroll
-          for (int w = 0; w < W; ++w) qf[nb][i * W + w] = reinterpret_cast<const uint32_t*>(e)[w];
+            for (int w = 0; w < W; ++w) qf[nb][i * W + w] = v[w];
+          }
         }
-      }
+      };
       const float srow = a.k_scale ? sc * a.k_scale[kh] : sc;
 
       const char* kb = static_cast<const char*>(a.k) + kh * a.k_head * (int64_t)sizeof(C);
@@ -276,51 +481,60 @@ __global__ __launch_bounds__(kBlock, OCC) void kv_attention_kernel(KvAttentionAr
       const int32_t* table = a.table + r * a.table_stride;
 
       uint32_t kr[TS][S::KL][4], vr[S::NT][S::NC][S::VW];
-      // Loads of one step; returns the mask of its visible tokens (all zero past the row).
+      // Where a step's tokens are, in two halves: its pages, fetched two steps ahead
+      // of the loads that need them, and the addresses and visible tokens they give.
+      struct Pages {
+        int32_t t0;              // the step's first token
+        int32_t page[PAGED16 ? TS : 1];
+      };
       struct Where {
-        uint32_t mask;
-        int64_t off[2];          // PAGED16: unused; else this lane's token's offsets in bytes
-        const char* k[TS];
+        uint32_t mask;           // visible tokens
+        int64_t off[2];          // not PAGED16: this lane's token's offsets in bytes
+        const char* k[TS];       // PAGED16: the tiles' first keys and values
         const char* v[TS];
       };
-      auto locate = [&](int32_t step) {
+      auto fetch = [&](int32_t step) {
+        Pages f;
+        const int32_t i = uniform(min(step, x.steps - 1));
+        f.t0 = (i < x.s0 ? i : x.s1 + i - x.s0) * ST;
+        if (PAGED16) {
+#pragma unroll
+          for (int ts = 0; ts < TS; ++ts) {
+            const int32_t tt = min(f.t0 + 16 * ts, x.n - 1);
+            f.page[ts] = scalar_load(table, div_by((uint32_t)tt, a.page));
+          }
+        } else {
+          const int32_t t = min(f.t0 + (lane & (ST - 1)), x.n - 1);
+          f.page[0] = table[div_by((uint32_t)t, a.page)];
+        }
+        return f;
+      };
+      auto locate = [&](Pages f) {
         Where w;
-        const int32_t i = step < x.steps ? step : 0;
-        const int32_t t0 = (i < x.s0 ? i : x.s1 + i - x.s0) * ST;
+        f.t0 = uniform(f.t0);
+        const int32_t t = f.t0 + (lane & (ST - 1));
+        bool see = t < x.n && (t >= x.from || t < x.first);
         if (PAGED16) {
           bool ok[TS];
 #pragma unroll
           for (int ts = 0; ts < TS; ++ts) {
-            const int32_t tt = t0 + 16 * ts;
-            int32_t page = -1;
-            const uint32_t j = div_by((uint32_t)tt, a.page);
-            if (tt < x.n)
-              page = __builtin_amdgcn_readfirstlane(table[j]);
+            // past the row's end the page is that of its last token: masked, and inside
+            const int32_t page = uniform(f.page[ts]), tt = f.t0 + 16 * ts;
             ok[ts] = (uint32_t)page < (uint32_t)a.n_pages;
-            const int64_t p = ok[ts] ? page : 0, at = tt - (int32_t)(j * a.page.d);
+            const int64_t p = ok[ts] ? page : 0;
+            const int64_t at = tt - (int32_t)(div_by((uint32_t)tt, a.page) * a.page.d);
             w.k[ts] = kb + (p * a.k_page + at * a.k_token) * (int64_t)sizeof(C);
             w.v[ts] = vb + (p * a.v_page + at * a.v_token) * (int64_t)sizeof(C);
           }
-          const int32_t t = t0 + lane;
-          bool see = lane < ST && t < x.n && (t >= x.from || t < x.first);
-          see = see && (TS == 1 || lane < 16 ? ok[0] : ok[TS - 1]);
-          w.mask = (uint32_t)__ballot(see);
+          see = see && (TS == 1 || (lane & 16) == 0 ? ok[0] : ok[TS - 1]);
         } else {
-          const int32_t t = t0 + (lane & (ST - 1));
-          bool see = t < x.n && (t >= x.from || t < x.first);
-          int64_t page = 0, at = 0;
-          if (see) {
-            const uint32_t j = div_by((uint32_t)t, a.page);
-            const int32_t p = table[j];
-            see = (uint32_t)p < (uint32_t)a.n_pages;
-            page = see ? p : 0;
-            at = see ? t - (int32_t)(j * a.page.d) : 0;
-          }
-          w.off[0] = (page * a.k_page + at * a.k_token) * (int64_t)sizeof(C);
-          w.off[1] = (page * a.v_page + at * a.v_token) * (int64_t)sizeof(C);
-          w.mask = (uint32_t)(__ballot(see) & ((uint64_t(1) << ST) - 1));
+          see = see && (uint32_t)f.page[0] < (uint32_t)a.n_pages;
+          const int64_t p = see ? f.page[0] : 0;
+          const int64_t at = see ? t - (int32_t)(div_by((uint32_t)t, a.page) * a.page.d) : 0;
+          w.off[0] = (p * a.k_page + at * a.k_token) * (int64_t)sizeof(C);
+          w.off[1] = (p * a.v_page + at * a.v_token) * (int64_t)sizeof(C);
         }
-        if (step >= x.steps) w.mask = 0;
+        w.mask = (uint32_t)(__ballot(see) & ((uint64_t(1) << ST) - 1));
         return w;
       };
       auto load_k = [&](const Where& w) {
@@ -334,7 +548,7 @@ __global__ __launch_bounds__(kBlock, OCC) void kv_attention_kernel(KvAttentionAr
 #pragma unroll
           for (int i = 0; i < S::KL; ++i) {
             if (EXACT || i * (64 / (int)sizeof(C)) + g * (16 / (int)sizeof(C)) < D) {
-              const u32x4 v = *reinterpret_cast<const u32x4*>(p + i * 64);
+              const u32x4 v = ld_stream(reinterpret_cast<const u32x4*>(p + i * 64));
 #pragma unroll
               for (int e = 0; e < 4; ++e) kr[ts][i][e] = v[e];
             } else {
@@ -356,15 +570,15 @@ __global__ __launch_bounds__(kBlock, OCC) void kv_attention_kernel(KvAttentionAr
           for (int n = 0; n < S::NC; ++n) {
             if (EXACT || n * 16 * S::EV + c * S::EV < D) {
               if constexpr (S::VW == 4) {
-                const u32x4 v = *reinterpret_cast<const u32x4*>(p + n * 16 * S::VW * 4);
+                const u32x4 v = ld_stream(reinterpret_cast<const u32x4*>(p + n * 64 * S::VW));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) vr[t][n][e] = v[e];
               } else if constexpr (S::VW == 2) {
-                const u32x2 v = *reinterpret_cast<const u32x2*>(p + n * 16 * S::VW * 4);
+                const u32x2 v = ld_stream(reinterpret_cast<const u32x2*>(p + n * 64 * S::VW));
                 vr[t][n][0] = v[0];
                 vr[t][n][1] = v[1];
               } else {
-                vr[t][n][0] = *reinterpret_cast<const uint32_t*>(p + n * 16 * S::VW * 4);
+                vr[t][n][0] = ld_stream(reinterpret_cast<const uint32_t*>(p + n * 64 * S::VW));
               }
             } else {
 #pragma unroll
@@ -386,16 +600,23 @@ __global__ __launch_bounds__(kBlock, OCC) void kv_attention_kernel(KvAttentionAr
           for (int e = 0; e < S::EV; ++e) acc[nb][n][e] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
 
-      const int32_t step_end = min(tb * kWavesPerBlock, x.steps);
-      int32_t step = ta0 * kWavesPerBlock + wave;
-      if (step < step_end) {
-        Where now = locate(step);
+      const int32_t step_end = min(ub << a.step_shift, x.steps);
+      int32_t step = (ua << a.step_shift) + wave;
+      if (uniform(step) < step_end) {
+        const Pages first = fetch(step);
+        Pages ahead = fetch(step + kKvWaves);
+        if (a.q_aligned)
+          load_q(std::true_type());
+        else
+          load_q(std::false_type());
+        Where now = locate(first);
         load_k(now);
         load_v(now);
         for (;;) {
-          const int32_t next = step + kWavesPerBlock;
-          const bool more = next < step_end;
-          const Where then = locate(more ? next : step);
+          const int32_t next = step + kKvWaves;
+          const bool more = uniform(next) < step_end;
+          const Where then = locate(ahead);
+          ahead = fetch(next + kKvWaves);
 
           // S = K Q^T: score of token 16 ts + 4g + i with query column c
           f32x4 s[NB][TS];
@@ -445,6 +666,7 @@ __global__ __launch_bounds__(kBlock, OCC) void kv_attention_kernel(KvAttentionAr
           }
           if (more) load_k(then);
 
+          now.mask = (uint32_t)uniform((int32_t)now.mask);
           const bool full = now.mask == (ST == 32 ? 0xffffffffu : 0xffffu);
           // bit 16 ts + i: this lane's token of tile ts is visible
           const uint32_t vis = full ? 0xffffffffu : now.mask >> (4 * g);
@@ -594,7 +816,7 @@ __global__ __launch_bounds__(kBlock, OCC) void kv_attention_kernel(KvAttentionAr
         const int row = nb * 16 + c;
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWavesPerBlock; ++w) top = fmaxf(top, wave_m[w][row]);
+        for (int w = 0; w < kKvWaves; ++w) top = fmaxf(top, wave_m[w][row]);
         const float keep = __builtin_amdgcn_exp2f(m[nb] - (top == -INFINITY ? 0.f : top));
         if (row < rows) {
 #pragma unroll
@@ -616,137 +838,222 @@ __global__ __launch_bounds__(kBlock, OCC) void kv_attention_kernel(KvAttentionAr
       auto row_m = [&](int row) {
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWavesPerBlock; ++w) top = fmaxf(top, wave_m[w][row]);
+        for (int w = 0; w < kKvWaves; ++w) top = fmaxf(top, wave_m[w][row]);
         return top;
       };
       auto row_l = [&](int row, float top) {
         const float base = top == -INFINITY ? 0.f : top;
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWavesPerBlock; ++w)
+        for (int w = 0; w < kKvWaves; ++w)
           sum += wave_l[w][row] * __builtin_amdgcn_exp2f(wave_m[w][row] - base);
         return sum;
       };
       auto row_o = [&](int row, int d) {
         f32x4 o = *reinterpret_cast<const f32x4*>(&red[0][row][d]);
 #pragma unroll
-        for (int w = 1; w < kWavesPerBlock; ++w)
+        for (int w = 1; w < kKvWaves; ++w)
           o += *reinterpret_cast<const f32x4*>(&red[w][row][d]);
         return o;
       };
-      const float vscale = a.v_scale ? a.v_scale[kh] : 1.f;
-      auto write = [&](int row, int d, f32x4 o, float top, float sum) {
-        Q* out = static_cast<Q*>(a.out) + r * a.out_request + (q_head0 + row) * a.out_head + d;
-        const float inv = sum == 0.f ? 0.f : vscale / sum;
-        alignas(16) Q y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = from_f32<Q>(sum == 0.f ? 0.f : o[e] * inv);
-        if (a.out_aligned) {
-          if constexpr (sizeof(Q) == 4)
-            *reinterpret_cast<u32x4*>(out) = *reinterpret_cast<const u32x4*>(y);
-          else
-            *reinterpret_cast<u32x2*>(out) = *reinterpret_cast<const u32x2*>(y);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) out[e] = y[e];
-        }
-        if (a.lse && d == 0)
-          a.lse[(int64_t)r * a.n_kv_heads * a.group + q_head0 + row] =
-              sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
-      };
       const int quads = D / 4;
       if (whole) {
-        for (int i = tid; i < rows * quads; i += kBlock) {
+        const float vscale = a.v_scale ? a.v_scale[kh] : 1.f;
+        for (int i = tid; i < rows * quads; i += kKvBlock) {
           const int row = i / quads, d = (i - row * quads) * 4;
           const float top = row_m(row);
-          write(row, d, row_o(row, d), top, row_l(row, top));
+          kv_write<Q>(a, r, q_head0 + row, d, row_o(row, d), top, row_l(row, top), vscale);
         }
       } else {
-        // slot 2b: workgroup b's part of a row that began before it; 2b + 1: of one that
-        // goes on after it
-        int32_t* counters = static_cast<int32_t*>(a.workspace);
-        float* slots = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kKvCounterBytes);
-        constexpr int64_t SLOT = (int64_t)kv_slot_floats(NB, DPAD);
-        const int64_t b0 = (row_at + 1) / per, b1 = (row_at + cost - 1) / per;   // first, last part
-        auto slot_of = [&](int64_t b) { return slots + (2 * b + (b == b0 ? 1 : 0)) * SLOT; };
-        float* slot = slot_of(blockIdx.x);
-        for (int i = tid; i < rows * quads; i += kBlock) {
+        const KvCut cut{r, hc, steps_at, units};
+        const bool began_before = ua > 0;
+        if (began_before)
+          head_cut = cut;
+        else
+          tail_cut = cut;
+        float* slot = slots + (2 * blockIdx.x + (began_before ? 0 : 1)) * SLOT;
+        for (int i = tid; i < rows * quads; i += kKvBlock) {
           const int row = i / quads, d = (i - row * quads) * 4;
-          *reinterpret_cast<f32x4*>(slot + 2 * ROWS + row * DPAD + d) = row_o(row, d);
+          share4(slot + 2 * ROWS + row * DPAD + d, row_o(row, d));
           if (d == 0) {
             const float top = row_m(row);
-            slot[row] = top;
-            slot[ROWS + row] = row_l(row, top);
-          }
-        }
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) {
-          const int32_t seen = __hip_atomic_fetch_add(counters + b0, 1, __ATOMIC_ACQ_REL,
-                                                      __HIP_MEMORY_SCOPE_AGENT);
-          last_one = seen == (int32_t)(b1 - b0);
-          // the next call finds it as this one did
-          if (last_one) __hip_atomic_store(counters + b0, 0, __ATOMIC_RELAXED,
-                                           __HIP_MEMORY_SCOPE_AGENT);
-        }
-        __syncthreads();
-        if (last_one) {
-          __threadfence();
-          for (int i = tid; i < rows * quads; i += kBlock) {
-            const int row = i / quads, d = (i - row * quads) * 4;
-            float top = -INFINITY;
-            for (int64_t b = b0; b <= b1; ++b) top = fmaxf(top, slot_of(b)[row]);
-            const float base = top == -INFINITY ? 0.f : top;
-            float sum = 0.f;
-            f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-            for (int64_t b = b0; b <= b1; ++b) {
-              const float* s = slot_of(b);
-              const float w = __builtin_amdgcn_exp2f(s[row] - base);
-              sum += s[ROWS + row] * w;
-              o += *reinterpret_cast<const f32x4*>(s + 2 * ROWS + row * DPAD + d) * w;
-            }
-            write(row, d, o, top, sum);
+            share(slot + row, top);
+            share(slot + ROWS + row, row_l(row, top));
           }
         }
       }
-      __syncthreads();                           // red, wave_m and last_one are free again
+      __syncthreads();                           // red and wave_m are free again
     }
-    request_at += (int64_t)cost * heads;
-    if (request_at >= d1 || r + 1 >= a.n_requests) return;
+    row_before = request_at + cost * heads;
+    more_rows = row_before < d1 && r + 1 < a.n_requests;
+  }
+  if (a.join_apart) return;
+
+  // ---- rows cut at this run's ends: told, and joined where this is the last part
+  // (told only here, when the stores of both have long been under way)
+  int32_t* counters = static_cast<int32_t*>(a.workspace);
+  KvJoin h = kv_join_of(shares, head_cut), t = kv_join_of(shares, tail_cut);
+  wait_vmem();                                   // this wavefront's stores are done
+  __syncthreads();
+  if (tid == 0) {
+    const int32_t b = blockIdx.x;
+    last_one[0] = head_cut.r >= 0 && arrive(counters + h.counter(b), h.in_group(b));
+    last_one[1] = tail_cut.r >= 0 && arrive(counters + t.counter(b), t.in_group(b));
+  }
+  __syncthreads();
+  memory_order_point();
+#pragma unroll 1
+  for (int end = 0; end < 2; ++end) {
+    if (!uniform(last_one[end])) continue;
+    const KvCut cut = end ? tail_cut : head_cut;
+    const KvJoin j = end ? t : h;
+    const int kh = cut.hc / chunks, first_head = (cut.hc - kh * chunks) * ROWS;
+    const int rows = min(ROWS, a.group - first_head), quads = D / 4;
+    const int32_t group = j.group(blockIdx.x);
+    int32_t from = j.b0 + group * j.per_group, by = 1, many = j.in_group(blockIdx.x);
+    bool final = j.groups == 1, last = true;
+    while (last) {
+      float* first = slots + j.slot(from) * SLOT;          // takes the group's result
+      for (int i = tid; i < rows * quads; i += kKvBlock) {
+        const int row = i / quads, d = (i - row * quads) * 4;
+        const KvPart p = kv_join<ROWS, DPAD>(slots, j, from, by, many, row, d);
+        if (final) {
+          kv_write<Q>(a, cut.r, (int64_t)kh * a.group + first_head + row, d, p.o, p.m, p.l,
+                      a.v_scale ? a.v_scale[kh] : 1.f);
+        } else {
+          share4(first + 2 * ROWS + row * DPAD + d, p.o);
+          if (d == 0) {
+            wave_m[0][row] = p.m;
+            wave_l[0][row] = p.l;
+          }
+        }
+      }
+      if (final) break;
+      __syncthreads();                           // every thread has read the part's m and l
+      if (tid < rows) {
+        share(first + tid, wave_m[0][tid]);
+        share(first + ROWS + tid, wave_l[0][tid]);
+      }
+      wait_vmem();
+      __syncthreads();
+      if (tid == 0)
+        last_one[2] = arrive(counters + 2 * kKvMaxBlocks + j.slot(j.b0), j.groups);
+      __syncthreads();
+      memory_order_point();
+      last = uniform(last_one[2]) != 0;
+      from = j.b0;
+      by = j.per_group;
+      many = j.groups;
+      final = true;
+    }
+    __syncthreads();                             // wave_m and last_one are free again
   }
 #endif
 }
 
-// How many workgroups of one instantiation a CU holds: what its registers and
-// LDS leave.
-template <typename C, int DPAD, int NB>
-constexpr int kv_occupancy() {
-  return NB == 2 ? (DPAD == 256 ? 1 : 2) : DPAD == 256 || (sizeof(C) == 4 && DPAD > 64) ? 1 : 2;
+// The join as a launch of its own, for few rows that are cut into many parts
+// (kv_attention_kernel with join_apart leaves them all): one workgroup per
+// request and query head, its threads the quads of elements times 256 / quads
+// shares of the parts, which LDS adds in a fixed order.
+template <typename C, typename Q, int DPAD, int NB>
+__global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs a, uint32_t most) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef KvShape<C, Q, DPAD, NB> S;
+  constexpr int ROWS = 16 * NB, QUADS = DPAD / 4, SHARES = 256 / QUADS;
+  __shared__ __align__(16) float part_o[SHARES][QUADS][4];
+  __shared__ float part_m[SHARES], part_l[SHARES];
+  const int tid = threadIdx.x, lane = lane_id();
+  const int q_heads = a.n_kv_heads * a.group;
+  const int r = blockIdx.x / q_heads, q_head = blockIdx.x - r * q_heads;
+  const int kh = q_head / a.group, in_group = q_head - kh * a.group;
+  const int chunks = (a.group + ROWS - 1) / ROWS, heads = a.n_kv_heads * chunks;
+  const int hc = kh * chunks + in_group / ROWS, row = in_group % ROWS;
+
+  // every wavefront adds the costs up by itself: at most 64 requests
+  const int32_t cost = lane < a.n_requests
+                           ? kv_cost(kv_units(a, kv_span<S::ST>(a, a.lengths[lane]))) : 0;
+  int32_t total = cost, before = lane < r ? cost : 0;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    total += __shfl_xor(total, d);
+    before += __shfl_xor(before, d);
+  }
+  const KvShares shares = kv_shares(uniform(total) * heads, most);
+  const int32_t units = kv_units(a, kv_span<S::ST>(a, scalar_load(a.lengths, r)));
+  const int32_t row_cost = kv_cost(units);
+  const KvJoin j = kv_join_of(
+      shares, KvCut{r, hc, uniform(before) * heads + (hc + 1) * row_cost - units, units});
+  if (units == 0 || j.b0 == j.b1) return;        // written by its only part
+
+  const float* slots = reinterpret_cast<const float*>(static_cast<const char*>(a.workspace) +
+                                                      kKvCounterBytes);
+  const int quad = tid % QUADS, share = tid / QUADS;
+  const int32_t parts = j.b1 - j.b0 + 1;
+  KvPart p{-INFINITY, 0.f, f32x4{0.f, 0.f, 0.f, 0.f}};
+  if (share < parts)
+    p = kv_join<ROWS, DPAD>(slots, j, j.b0 + share, SHARES, (parts - share + SHARES - 1) / SHARES,
+                            row, quad * 4);
+  *reinterpret_cast<f32x4*>(part_o[share][quad]) = p.o;
+  if (quad == 0) {
+    part_m[share] = p.m;
+    part_l[share] = p.l;
+  }
+  __syncthreads();
+  if (tid < a.head_dim / 4) {
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < SHARES; ++i) top = fmaxf(top, part_m[i]);
+    const float base = top == -INFINITY ? 0.f : top;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < SHARES; ++i) {
+      const float w = __builtin_amdgcn_exp2f(part_m[i] - base);
+      sum += part_l[i] * w;
+      o += *reinterpret_cast<const f32x4*>(part_o[i][tid]) * w;
+    }
+    kv_write<Q>(a, r, q_head, tid * 4, o, top, sum, a.v_scale ? a.v_scale[kh] : 1.f);
+  }
+#endif
 }
 
 template <typename C, typename Q, int DPAD, int NB>
-hipError_t launch_kv_attention_shape(const KvAttentionArgs& a, hipStream_t s) {
-  constexpr int OCC = kv_occupancy<C, DPAD, NB>();
+hipError_t launch_kv_attention_shape(KvAttentionArgs a, hipStream_t s) {
+  // Workgroups per CU, all resident at once (what registers and LDS leave):
+  // the runs are equal, so a grid of more would only be cut finer. Twice as
+  // many workgroups took 3% longer on 2.3 GB and 10% on 190 MB; three waves a
+  // SIMD, where the registers of a type allow them, were no faster.
+  constexpr int OCC = DPAD == 256 ? 1 : 2;
   const int chunks = (a.group + 16 * NB - 1) / (16 * NB);
-  // no more workgroups than units: tiles at the table's full width, and one a row
+  // no more workgroups than units at the table's full width
   const int64_t steps = a.table_tokens / KvShape<C, Q, DPAD, NB>::ST + 3;
-  const int64_t units = (int64_t)a.n_requests * a.n_kv_heads * chunks * (steps / 4 + 2);
-  const int64_t most = (int64_t)a.n_cus * OCC < kKvMaxBlocks ? a.n_cus * OCC : kKvMaxBlocks;
-  const int64_t want = (units + a.min_share - 1) / a.min_share;
-  const unsigned blocks = (unsigned)(want < most ? want : most);
+  const int64_t rows = (int64_t)a.n_requests * a.n_kv_heads * chunks;
+  a.step_shift = 0;
+  while (rows * ((steps >> a.step_shift) + 1 + kKvRowCost) > (int64_t(1) << 30)) ++a.step_shift;
+  const int64_t units = rows * ((steps >> a.step_shift) + 1 + kKvRowCost);
+  const int64_t most = kKvCus * OCC;
+  const unsigned blocks = (unsigned)std::min(std::max<int64_t>(units / kKvMinRun, 1), most);
+  // Rows that can be cut into more than kKvFlatJoin parts each are joined by a
+  // second launch that spreads the join over workgroups: 290 MB of two long
+  // requests with two key heads take 65 us so, 79 us joined by the workgroups
+  // that come last.
+  a.join_apart = a.n_requests <= kWave && rows * kKvFlatJoin <= most &&
+                 units / rows > kKvFlatJoin * kKvMinRun;
   // one page for each 16 tokens, and lane offsets within them in 32 bits
   const bool paged16 = a.page.d % 16 == 0 && a.k_token < (int64_t(1) << 24) &&
                        a.v_token < (int64_t(1) << 24);
   if (!paged16)
     hipLaunchKernelGGL((kv_attention_kernel<C, Q, DPAD, NB, false, false, OCC>), dim3(blocks),
-                       dim3(kBlock), 0, s, a);
+                       dim3(kKvBlock), 0, s, a);
   else if (a.head_dim == DPAD)
     hipLaunchKernelGGL((kv_attention_kernel<C, Q, DPAD, NB, true, true, OCC>), dim3(blocks),
-                       dim3(kBlock), 0, s, a);
+                       dim3(kKvBlock), 0, s, a);
   else
     hipLaunchKernelGGL((kv_attention_kernel<C, Q, DPAD, NB, false, true, OCC>), dim3(blocks),
-                       dim3(kBlock), 0, s, a);
+                       dim3(kKvBlock), 0, s, a);
+  if (a.join_apart)
+    hipLaunchKernelGGL((kv_attention_join_kernel<C, Q, DPAD, NB>),
+                       dim3((unsigned)(a.n_requests * a.n_kv_heads * a.group)), dim3(256), 0, s, a,
+                       blocks);
   return hipGetLastError();
 }
 

@@ -79,8 +79,8 @@ struct KvAttentionArgs {
   int32_t n_requests, n_kv_heads, group, head_dim;   // group: query heads per key head
   int32_t window, sinks;       // window 0: all tokens
   int32_t cache_dtype, dtype;
-  int32_t min_share;           // least units (tiles and rows) of one workgroup
-  int32_t n_cus;
+  int32_t step_shift;          // set by the launch: see kv_units
+  bool join_apart;             // set by the launch: a second one joins the cut rows
   bool q_aligned, out_aligned; // 16-byte loads of q, four-element stores of out
   float scale;
   FastDiv page;

@@ -15,7 +15,7 @@ from typing import Optional
 import torch
 
 from . import binding
-from .binding import _check, _stream
+from .binding import _check, _stream as _given_stream
 
 KV_F32, KV_F16, KV_BF16, KV_F8E4M3 = 0, 1, 2, 3
 KV_DTYPE = {torch.float32: KV_F32, torch.float16: KV_F16, torch.bfloat16: KV_BF16,
@@ -58,17 +58,33 @@ def _load():
     return _lib
 
 
+# The current stream's handle without a Stream object: torch.cuda.current_stream() takes
+# 2.7 us, more than all the rest of a call's marshalling.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, t):
+    """hipStream_t of `stream`, or of the current stream of t's device."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _given_stream(stream)
+
+
+_I32 = torch.int32
+
+
 def _ints(t, name: str, n: int) -> int:
     """Pointer of a contiguous device int32 tensor of at least n entries."""
+    if (isinstance(t, torch.Tensor) and t.dtype is _I32 and t.is_cuda and t.is_contiguous()
+            and t.numel() >= n):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
         raise TypeError("%s must be an int32 tensor" % name)
     if not t.is_cuda:
         raise ValueError("%s must be a device (cuda) tensor" % name)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if t.numel() < n:
-        raise ValueError("%s has %d entries, %d are needed" % (name, t.numel(), n))
-    return t.data_ptr()
+    raise ValueError("%s has %d entries, %d are needed" % (name, t.numel(), n))
 
 
 def _table(t, n_requests: int):
@@ -94,19 +110,27 @@ def _on(stream):
 
 
 def _rows(t, name: str, shape):
-    """Pointer and the two outer strides of a device tensor [n, heads, head_dim] with a
-    unit last stride; a size that is None may be anything."""
+    """Pointer and the two outer strides of a device tensor of this shape [n, heads,
+    head_dim] with a unit last stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
     if not t.is_cuda:
         raise ValueError("%s must be a device (cuda) tensor" % name)
-    if t.dim() != 3 or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError("%s must have shape %s, not %s"
-                         % (name, tuple("*" if w is None else w for w in shape), tuple(t.shape)))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
     s0, s1, s2 = t.stride()
-    if s2 != 1 and t.shape[2] > 1:
+    if s2 != 1 and shape[2] > 1:
         raise ValueError("%s must have a unit last stride" % name)
     return t.data_ptr(), s0, s1
+
+
+def _outer(t, name: str) -> int:
+    """Size of the first dimension of a 3-D tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dim() != 3:
+        raise ValueError("%s must be 3-D, not %s" % (name, tuple(t.shape)))
+    return t.shape[0]
 
 
 def spmv_kv_grow(lengths, n_new, page_size: int, free_pages, cursor, table, lengths_out,
@@ -126,7 +150,7 @@ def spmv_kv_grow(lengths, n_new, page_size: int, free_pages, cursor, table, leng
         tp, ts, tw, _ints(lengths_out, "lengths_out", n), _ints(cursor_out, "cursor_out", 1),
         _ints(token_ptr, "token_ptr", n + 1), _ints(slots, "slots", 0),
         None if positions is None else _ints(positions, "positions", n_tokens), n_tokens,
-        _ints(status, "status", 2), _stream(stream)), "spmv_kv_grow")
+        _ints(status, "status", 2), _stream(stream, status)), "spmv_kv_grow")
 
 
 def spmv_kv_shrink(lengths, keep, page_size: int, free_pages, cursor, table, lengths_out,
@@ -140,7 +164,7 @@ def spmv_kv_shrink(lengths, keep, page_size: int, free_pages, cursor, table, len
         n, _ints(lengths, "lengths", n), _ints(keep, "keep", n), page_size,
         _ints(free_pages, "free_pages", 0), free_pages.numel(), _ints(cursor, "cursor", 1),
         tp, ts, tw, _ints(lengths_out, "lengths_out", n), _ints(cursor_out, "cursor_out", 1),
-        _ints(status, "status", 2), _stream(stream)), "spmv_kv_shrink")
+        _ints(status, "status", 2), _stream(stream, status)), "spmv_kv_shrink")
 
 
 class KvCache:
@@ -187,13 +211,14 @@ class KvCache:
     def append(self, k, v, slots, stream=None) -> None:
         """Write k[t], v[t] ([n_tokens, n_kv_heads, head_dim]) to slot slots[t] for every
         token; slots outside the cache (-1) are skipped."""
-        kp, k0, k1 = _rows(k, "k", (None, self.n_heads, self.head_dim))
-        vp, v0, v1 = _rows(v, "v", k.shape)
+        n = _outer(k, "k")
+        shape = (n, self.n_heads, self.head_dim)
+        kp, k0, k1 = _rows(k, "k", shape)
+        vp, v0, v1 = _rows(v, "v", shape)
         if k.dtype != v.dtype or k.dtype not in KV_DTYPE:
             raise TypeError("k and v must have one dtype of %s" % (tuple(KV_DTYPE),))
-        n = k.shape[0]
         _check(_load().spmv_kv_append(self._ref, n, kp, k0, k1, vp, v0, v1, KV_DTYPE[k.dtype],
-                                      _ints(slots, "slots", n), _stream(stream)),
+                                      _ints(slots, "slots", n), _stream(stream, slots)),
                "spmv_kv_append")
 
     def workspace_size(self, n_q_heads: int) -> int:
@@ -214,12 +239,16 @@ class KvCache:
         newest token counted. window 0 sees every token, otherwise the last ``window`` and
         the first ``sinks``. scale: head_dim ** -0.5 unless given. lse: float32
         [n_requests, n_q_heads] to receive the log of the softmax's sum. Returns out."""
-        qp, q0, q1 = _rows(q, "q", (None, None, self.head_dim))
-        n, heads = q.shape[0], q.shape[1]
+        n = _outer(q, "q")
+        shape = q.shape
+        heads = shape[1]
+        if shape[2] != self.head_dim:
+            raise ValueError("q must be [n_requests, n_q_heads, %d]" % self.head_dim)
+        qp, q0, q1 = _rows(q, "q", shape)
         if out is None:
             with _on(stream):
                 out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        op, o0, o1 = _rows(out, "out", q.shape)
+        op, o0, o1 = _rows(out, "out", shape)
         if q.dtype not in KV_DTYPE or out.dtype != q.dtype:
             raise TypeError("q and out must have one dtype of %s" % (tuple(KV_DTYPE),))
         tp, ts, tw = _table(table, n)
@@ -232,7 +261,7 @@ class KvCache:
                                  % (n * heads))
             lp = lse.data_ptr()
         need = self.workspace_size(heads)
-        handle = _stream(stream)
+        handle = _stream(stream, q)
         if workspace is None:
             workspace = self._ws.get(handle)
             if workspace is None or workspace.numel() < need:
