@@ -371,7 +371,7 @@ __global__ __launch_bounds__(kKvBlock, OCC) void kv_attention_kernel(KvAttention
   __shared__ __align__(16) float red[kKvWaves][ROWS][PITCH];
   __shared__ float wave_m[kKvWaves][ROWS], wave_l[kKvWaves][ROWS];
   __shared__ int32_t scan[kKvWaves];
-  __shared__ int32_t found_row, found_before, last_one[3];
+  __shared__ int32_t found[3], last_one[2];
 
   const int tid = threadIdx.x, lane = lane_id(), c = lane & 15, g = lane >> 4;
   const int wave = uniform(tid / kWave);
@@ -406,17 +406,18 @@ __global__ __launch_bounds__(kKvBlock, OCC) void kv_attention_kernel(KvAttention
   const int32_t d0 = kv_begin(shares, blockIdx.x), d1 = kv_begin(shares, blockIdx.x + 1);
   if (before <= d0 && d0 < before + mine) {
     int r = r0;
+    int32_t length;
     for (;; ++r) {
-      const int32_t cost = kv_cost(kv_units(a, kv_span<ST>(a, a.lengths[r]))) * heads;
+      length = a.lengths[r];
+      const int32_t cost = kv_cost(kv_units(a, kv_span<ST>(a, length))) * heads;
       if (d0 < before + cost) break;
       before += cost;
     }
-    found_row = r;
-    found_before = before;
+    found[0] = r;
+    found[1] = before;                           // unit at which request r begins
+    found[2] = length;
   }
   __syncthreads();
-  int row_r = found_row;
-  int32_t row_before = found_before;             // unit at which request row_r begins
 
   float* slots = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kKvCounterBytes);
   constexpr int64_t SLOT = (int64_t)kv_slot_floats(NB, DPAD);
@@ -426,10 +427,12 @@ __global__ __launch_bounds__(kKvBlock, OCC) void kv_attention_kernel(KvAttention
 
   // rows cut at this run's two ends: their numbers and units (-1: none)
   KvCut head_cut{-1, 0, 0, 0}, tail_cut{-1, 0, 0, 0};
-  for (bool more_rows = true; more_rows; ++row_r) {
+  int row_r = found[0];
+  int32_t row_before = found[1], row_length = found[2];
+  for (;;) {
     const int r = uniform(row_r);
     const int32_t request_at = uniform(row_before);
-    const KvSpan x = kv_span<ST>(a, scalar_load(a.lengths, r));
+    const KvSpan x = kv_span<ST>(a, uniform(row_length));
     const int32_t units = kv_units(a, x), cost = kv_cost(units);
     int hc0 = d0 > request_at ? (uint32_t)(d0 - request_at) / (uint32_t)cost : 0;
     for (; hc0 < heads; ++hc0) {
@@ -885,7 +888,9 @@ __global__ __launch_bounds__(kKvBlock, OCC) void kv_attention_kernel(KvAttention
       __syncthreads();                           // red and wave_m are free again
     }
     row_before = request_at + cost * heads;
-    more_rows = row_before < d1 && r + 1 < a.n_requests;
+    if (row_before >= d1 || r + 1 >= a.n_requests) break;
+    row_r = r + 1;
+    row_length = scalar_load(a.lengths, row_r);
   }
   if (a.join_apart) return;
 
@@ -895,58 +900,69 @@ __global__ __launch_bounds__(kKvBlock, OCC) void kv_attention_kernel(KvAttention
   KvJoin h = kv_join_of(shares, head_cut), t = kv_join_of(shares, tail_cut);
   wait_vmem();                                   // this wavefront's stores are done
   __syncthreads();
+  const int32_t b = blockIdx.x;
   if (tid == 0) {
-    const int32_t b = blockIdx.x;
     last_one[0] = head_cut.r >= 0 && arrive(counters + h.counter(b), h.in_group(b));
     last_one[1] = tail_cut.r >= 0 && arrive(counters + t.counter(b), t.in_group(b));
   }
   __syncthreads();
   memory_order_point();
-#pragma unroll 1
-  for (int end = 0; end < 2; ++end) {
-    if (!uniform(last_one[end])) continue;
-    const KvCut cut = end ? tail_cut : head_cut;
-    const KvJoin j = end ? t : h;
-    const int kh = cut.hc / chunks, first_head = (cut.hc - kh * chunks) * ROWS;
-    const int rows = min(ROWS, a.group - first_head), quads = D / 4;
-    const int32_t group = j.group(blockIdx.x);
-    int32_t from = j.b0 + group * j.per_group, by = 1, many = j.in_group(blockIdx.x);
-    bool final = j.groups == 1, last = true;
-    while (last) {
-      float* first = slots + j.slot(from) * SLOT;          // takes the group's result
-      for (int i = tid; i < rows * quads; i += kKvBlock) {
-        const int row = i / quads, d = (i - row * quads) * 4;
-        const KvPart p = kv_join<ROWS, DPAD>(slots, j, from, by, many, row, d);
-        if (final) {
-          kv_write<Q>(a, cut.r, (int64_t)kh * a.group + first_head + row, d, p.o, p.m, p.l,
-                      a.v_scale ? a.v_scale[kh] : 1.f);
-        } else {
-          share4(first + 2 * ROWS + row * DPAD + d, p.o);
-          if (d == 0) {
-            wave_m[0][row] = p.m;
-            wave_l[0][row] = p.l;
-          }
+  const int quads = D / 4;
+  auto rows_of = [&](const KvCut& c) {
+    return min(ROWS, a.group - (int32_t)((uint32_t)c.hc % (uint32_t)chunks) * ROWS);
+  };
+  const int rows_h = rows_of(head_cut), rows_t = rows_of(tail_cut);
+  // level 0: the parts of the groups that are complete; level 1: their groups. The items
+  // (rows times quads of elements) of both cut rows are dealt out together.
+  bool do_h = uniform(last_one[0]) != 0, do_t = uniform(last_one[1]) != 0;
+  for (int level = 0; do_h || do_t; ++level) {
+    const int items_h = do_h ? rows_h * quads : 0, items_t = do_t ? rows_t * quads : 0;
+    for (int i = tid; i < items_h + items_t; i += kKvBlock) {
+      const bool of_t = i >= items_h;
+      const KvCut& cut = of_t ? tail_cut : head_cut;
+      const KvJoin& j = of_t ? t : h;
+      const int item = of_t ? i - items_h : i, row = item / quads, d = (item - row * quads) * 4;
+      const int32_t from = level ? j.b0 : j.b0 + j.group(b) * j.per_group;
+      const KvPart p = kv_join<ROWS, DPAD>(slots, j, from, level ? j.per_group : 1,
+                                           level ? j.groups : j.in_group(b), row, d);
+      if (level || j.groups == 1) {
+        const int kh = cut.hc / chunks;
+        const int64_t q_head = (int64_t)kh * a.group + (cut.hc - kh * chunks) * ROWS + row;
+        kv_write<Q>(a, cut.r, q_head, d, p.o, p.m, p.l,
+                    S::F8 && a.v_scale ? a.v_scale[kh] : 1.f);
+      } else {
+        // the group's first slot takes its result
+        share4(slots + j.slot(from) * SLOT + 2 * ROWS + row * DPAD + d, p.o);
+        if (d == 0) {
+          wave_m[of_t][row] = p.m;
+          wave_l[of_t][row] = p.l;
         }
       }
-      if (final) break;
-      __syncthreads();                           // every thread has read the part's m and l
-      if (tid < rows) {
-        share(first + tid, wave_m[0][tid]);
-        share(first + ROWS + tid, wave_l[0][tid]);
-      }
-      wait_vmem();
-      __syncthreads();
-      if (tid == 0)
-        last_one[2] = arrive(counters + 2 * kKvMaxBlocks + j.slot(j.b0), j.groups);
-      __syncthreads();
-      memory_order_point();
-      last = uniform(last_one[2]) != 0;
-      from = j.b0;
-      by = j.per_group;
-      many = j.groups;
-      final = true;
     }
-    __syncthreads();                             // wave_m and last_one are free again
+    do_h = do_h && h.groups > 1 && level == 0;
+    do_t = do_t && t.groups > 1 && level == 0;
+    if (!do_h && !do_t) break;
+    __syncthreads();                             // every thread has read the parts' m and l
+    for (int i = tid; i < 2 * ROWS; i += kKvBlock) {
+      const int end = i / ROWS, row = i - end * ROWS;
+      const KvJoin& j = end ? t : h;
+      if (end ? do_t && row < rows_t : do_h && row < rows_h) {
+        float* first = slots + j.slot(j.b0 + j.group(b) * j.per_group) * SLOT;
+        share(first + row, wave_m[end][row]);
+        share(first + ROWS + row, wave_l[end][row]);
+      }
+    }
+    wait_vmem();
+    __syncthreads();
+    if (tid == 0) {
+      int32_t* rows_counters = counters + 2 * kKvMaxBlocks;
+      last_one[0] = do_h && arrive(rows_counters + h.slot(h.b0), h.groups);
+      last_one[1] = do_t && arrive(rows_counters + t.slot(t.b0), t.groups);
+    }
+    __syncthreads();
+    memory_order_point();
+    do_h = uniform(last_one[0]) != 0;
+    do_t = uniform(last_one[1]) != 0;
   }
 #endif
 }
