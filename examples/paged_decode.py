@@ -1,0 +1,115 @@
+"""A serving loop over a paged cache: requests of unequal length enter with a
+prompt, one attention layer answers token by token, finished requests give
+their pages back and their rows to new ones.
+
+    python3 examples/paged_decode.py [--requests 32] [--steps 64] [--check]
+
+Per step and on the device only: pages for the new tokens and their slots
+(PageTable.grow), keys and values to those slots (KvCache.append), attention
+of the newest token of every request (KvCache.attend). The layer's weights
+and the tokens' embeddings are random; --check holds every answer against
+attention over the dense history in 64 bits.
+"""
+import argparse
+import math
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+import load_balanced_csr_amd as lb  # noqa: E402
+
+
+class Layer:
+    """One attention layer with n_q_heads query heads over n_kv_heads key heads."""
+
+    def __init__(self, width, n_q_heads, n_kv_heads, head_dim, dtype, g):
+        self.heads = (n_q_heads, n_kv_heads, n_kv_heads)
+        self.head_dim = head_dim
+        w = torch.randn(width, sum(self.heads) * head_dim, device="cuda", generator=g)
+        self.w_qkv = (w / math.sqrt(width)).to(dtype)
+
+    def qkv(self, x):
+        """Queries, keys and values [n, heads, head_dim] of embeddings [n, width]: views of
+        one product, whose strides the cache takes as they are."""
+        y = (x @ self.w_qkv).view(x.shape[0], sum(self.heads), self.head_dim)
+        return torch.split(y, self.heads, dim=1)
+
+
+def serve(requests=32, steps=64, width=512, n_q_heads=16, n_kv_heads=4, head_dim=64, page_size=16,
+          longest=400, dtype=torch.bfloat16, seed=0, check=False):
+    """Runs the loop; returns the answers of the last step, the number of requests that
+    ended, and the largest error found (None without check)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    host = torch.Generator().manual_seed(seed)
+    layer = Layer(width, n_q_heads, n_kv_heads, head_dim, dtype, g)
+    max_pages = -(-longest // page_size)
+    n_pages = requests * max_pages
+    pool = torch.empty(2, n_pages, page_size, n_kv_heads, head_dim, dtype=dtype, device="cuda")
+    cache = lb.KvCache(pool[0], pool[1])
+    pages = lb.PageTable(requests, max_pages, n_pages, page_size)
+
+    # the host's own view of the batch: how long each request is and will be
+    now = [0] * requests
+    goal = [0] * requests
+    history = [[] for _ in range(requests)]
+    ended, worst = 0, 0.0 if check else None
+    out = None
+    for _ in range(steps):
+        new, keep = [], []
+        for r in range(requests):
+            done = now[r] >= goal[r]
+            if done:                     # the row takes another request, prompt first
+                ended += goal[r] > 0
+                prompt = int(torch.randint(1, longest // 2, (1,), generator=host))
+                goal[r] = prompt + int(torch.randint(1, longest // 2, (1,), generator=host))
+                now[r], history[r] = 0, []
+            keep.append(now[r])
+            new.append(prompt if done else 1)
+        pages.shrink(torch.tensor(keep, dtype=torch.int32, device="cuda"))
+        n_tokens = sum(new)
+        slots, _ = pages.grow(torch.tensor(new, dtype=torch.int32, device="cuda"), n_tokens)
+
+        x = torch.randn(n_tokens, width, device="cuda", generator=g).to(dtype)
+        q, k, v = layer.qkv(x)
+        cache.append(k, v, slots)
+        last = pages.token_ptr[1:].long() - 1        # the newest token of each request
+        out = cache.attend(q[last], pages.table, pages.lengths)
+
+        at = 0
+        for r in range(requests):
+            now[r] += new[r]
+            if check:
+                history[r].append((k[at:at + new[r]], v[at:at + new[r]]))
+                dense = [torch.cat(t).double() for t in zip(*history[r])]
+                worst = max(worst, error(q[last[r]], *dense, out[r]))
+            at += new[r]
+    code, detail = pages.status                      # the one wait of the loop
+    if code != lb.KV_OK:
+        raise RuntimeError("the pool ran out: code %d, detail %d" % (code, detail))
+    return out, ended, worst
+
+
+def error(q, k, v, got):
+    """Relative error of one request's answer against dense attention in 64 bits."""
+    group = q.shape[0] // k.shape[1]
+    k, v = (t.repeat_interleave(group, dim=1).transpose(0, 1) for t in (k, v))
+    s = (k @ q.double()[:, :, None])[..., 0] / math.sqrt(q.shape[-1])
+    want = (torch.softmax(s, dim=1)[:, None, :] @ v)[:, 0]
+    return float((got.double() - want).norm() / want.norm())
+
+
+def main():
+    ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
+    ap.add_argument("--requests", type=int, default=32)
+    ap.add_argument("--steps", type=int, default=64)
+    ap.add_argument("--check", action="store_true")
+    a = ap.parse_args()
+    out, ended, worst = serve(a.requests, a.steps, check=a.check)
+    print("%d steps of %d requests, %d ended%s" % (
+        a.steps, a.requests, ended, "" if worst is None else ", largest error %.2g" % worst))
+
+
+if __name__ == "__main__":
+    main()

@@ -224,6 +224,31 @@ def test_offsets_past_32_bits():
     assert kv_ref.worst(out, want[0], want[2]) <= 1.0
 
 
+def test_tokens_far_apart_within_a_page():
+    """Tokens outermost in memory, 2^24 elements from one to the next."""
+    c = Case([50, 33, 16], Hq=4, H=1, D=64)
+    n_pages = 2 ** 18
+    want = c.ref()
+    caches = []
+    for t in (c.k, c.v):
+        far = torch.empty(16, n_pages, 1, 64, dtype=BF16, device="cuda").transpose(0, 1)
+        far[:t.shape[0]] = t.cuda()
+        caches.append(far)
+    assert caches[0].stride(1) == 2 ** 24
+    out = lb.KvCache(*caches).attend(c.q.cuda(), c.table.cuda(), c.lengths.cuda())
+    assert kv_ref.worst(out, want[0], want[2]) <= 1.0
+
+
+def test_a_table_as_wide_as_tables_get():
+    """2^31 - 2048 tokens of room in each of 20 rows: shares are dealt in several steps."""
+    c = Case([0, 1, 5000, 63, 64, 65, 300, 2, 1100, 1024] * 2, Hq=4, H=2, D=64, P=1024)
+    want = c.ref()
+    wide = torch.full((20, 2 ** 21 - 2), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.width] = c.table.cuda()
+    out = c.cache().attend(c.q.cuda(), wide, c.lengths.cuda())
+    assert kv_ref.worst(out, want[0], want[2]) <= 1.0
+
+
 def test_strided_queries_outputs_and_tables():
     c = Case([100, 3, 260, 64], Hq=6, H=3, D=80, dtype=F16)
     want = c.ref()

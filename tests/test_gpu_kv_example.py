@@ -1,0 +1,31 @@
+"""The serving loop of examples/paged_decode.py, small, each answer held
+against dense attention: block tables, appends and attention together, with
+requests that end and rows that are taken again."""
+import importlib.util
+import os
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def example():
+    spec = importlib.util.spec_from_file_location(
+        "paged_decode", os.path.join(ROOT, "examples", "paged_decode.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+@pytest.mark.parametrize("dtype,bound", [
+    # one rounding of the result to 8, 11 or 24 bits (2^-8, 2^-11, 2^-24 at most for each
+    # element), and for float32 sums over 400 tokens and 64 elements of scores below 16
+    (torch.bfloat16, 2.0 ** -8 + 2.0 ** -12), (torch.float16, 2.0 ** -11 + 2.0 ** -12),
+    (torch.float32, 2.0 ** -12)])
+def test_the_serving_loop(dtype, bound):
+    out, ended, worst = example().serve(requests=5, steps=40, width=128, n_q_heads=6, n_kv_heads=2,
+                                        longest=60, page_size=7, dtype=dtype, check=True)
+    assert out.shape == (5, 6, 64) and ended >= 5
+    assert worst <= bound, worst
