@@ -27,13 +27,27 @@
 // Rows of 32-bit elements need no transpose (one token per operand).
 //
 // Load balance. A row (request, key head, block of query heads) costs its
-// tiles (4 steps, one for each wavefront of a workgroup) plus one, and each
-// workgroup takes an equal run of the rows' costs laid end to end: the
-// merge-path split with rows and tiles as its units. Every workgroup finds its
-// run by a scan over the requests' lengths, so there is no planning launch.
-// Rows that a run cuts leave partial (m, l, o) in the workspace; the
-// workgroup that adds the last part (a counter per row) joins them in the
-// order of the row, so the bits do not depend on who is last.
+// steps and a few more for its beginning and end, and each workgroup takes an
+// equal run of the rows' costs laid end to end: the merge-path split with rows
+// and steps as its units. A run's steps of one row go to the workgroup's four
+// wavefronts in turn; LDS joins their parts. Every workgroup finds its run by
+// a scan over the requests' lengths, so there is no planning launch. Rows that
+// a run cuts leave partial (m, l, o) in the workspace; the workgroup that adds
+// the last part (a counter per row) joins them in the order of the row, so the
+// bits do not depend on who is last.
+//
+// Measured (keys and values of 128 elements in bf16, MI355X): 2.3 GB in 128
+// rows of 2048 to 8192 tokens and 8 key heads 366 us, 6.4 TB/s (a streaming
+// read reaches 7.0); 190 MB in 64 rows of 16 to 4096 tokens 42 us; one row of
+// 513 tokens 10 us. HBM reads are the rows' bytes and 1% (counted). Beside the
+// bytes a call costs about 10 us: launch 2, the scan and a first row's
+// addresses 2.5, the first loads 2, and at the end LDS, the parts' stores, the
+// counter and the join 3.5.
+// Looked at and not kept: loads of the next row begun under the last step of
+// the one before (3% slower: its coordinates do not fit the scalar registers
+// beside the row's), one key head for each wavefront (2% faster on large rows
+// of many heads, 4% slower on mixed ones, 15% on one short row), 64-token
+// steps for rows of 128 bytes (5% slower on 96 rows of 8-bit keys).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -181,6 +195,18 @@ struct KvShape {
   static constexpr int TS = F32 ? 1 : 2;              // 16-token tiles per step
   static constexpr int ST = 16 * TS;                  // tokens per step
   static constexpr int KL = DPAD * sizeof(C) / 64;    // 16-byte loads of a key per lane
+  // What a row costs beside its steps, in steps: about 100 tokens. (For 16-bit
+  // types 3 and 6 instead of 4 were 2% and 3% slower on 64 mixed rows; for
+  // 32-bit ones 4 instead of 6 was 8% slower on 17 short ones.)
+  static constexpr int ROW_COST = F32 ? 6 : 4;
+  // Runs of at least this many units are dealt to one workgroup per CU, shorter
+  // ones to two. 4 wavefronts of 16 KB a step keep enough in flight, and half
+  // as many places read at once suit the memory better: 2.3 GB of bf16 rows
+  // 366 us (6.4 TB/s) against 399 us, 293 MB of two long rows 63 against 66.
+  // Short runs need the second workgroup while the first begins and ends rows
+  // (190 MB in 64 rows: 42 us against 47), smaller steps always (8-bit rows:
+  // 83 us against 99).
+  static constexpr int LONG_RUN = 32 * TS * DPAD * (int)sizeof(C) >= 16384 ? 32 : 1 << 30;
   // elements of a value one lane loads at a time, and how often
   static constexpr int EV = F8 ? DPAD / 16 : F32 ? 4 : (DPAD >= 128 ? 8 : 4);
   static constexpr int NC = DPAD / (16 * EV);
@@ -216,22 +242,24 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttentionArgs& a, int32_t leng
 }
 // What a row costs, in units of one step (of 1 << step_shift steps where the
 // host has found that the rows' costs could pass 30 bits otherwise): its steps
-// and kKvRowCost for beginning and ending it, or one for a row without any.
-constexpr int32_t kKvRowCost = 4;
+// and ROW_COST for beginning and ending it, or one for a row without any.
 __device__ __forceinline__ int32_t kv_units(const KvAttentionArgs& a, const KvSpan& x) {
   return (int32_t)(((uint32_t)x.steps + (1u << a.step_shift) - 1) >> a.step_shift);
 }
+template <typename S>
 __device__ __forceinline__ int32_t kv_cost(int32_t units) {
-  return units > 0 ? units + kKvRowCost : 1;
+  return units > 0 ? units + S::ROW_COST : 1;
 }
 
 // The rows' units cut into runs, one for each workgroup, whose lengths differ
-// by one at most; none shorter than kKvMinRun, however few rows there are.
+// by one at most; none shorter than kKvMinRun, however few rows there are, and
+// one run per CU where they get long (LONG_RUN).
 struct KvShares {
   int32_t runs, base, longer;      // runs of base + 1 units, then of base
 };
-__device__ __forceinline__ KvShares kv_shares(int32_t total, uint32_t most) {
-  const int32_t runs = min((int32_t)most, max(total / kKvMinRun, 1));
+__device__ __forceinline__ KvShares kv_shares(int32_t total, uint32_t most, int32_t long_run) {
+  int32_t runs = min((int32_t)most, max(total / kKvMinRun, 1));
+  if (runs > kKvCus && (uint32_t)total / (uint32_t)runs >= (uint32_t)long_run) runs = kKvCus;
   return KvShares{runs, (int32_t)((uint32_t)total / (uint32_t)runs),
                   (int32_t)((uint32_t)total % (uint32_t)runs)};
 }
@@ -385,7 +413,7 @@ __global__ __launch_bounds__(kKvBlock, OCC) void kv_attention_kernel(KvAttention
   const int r1 = min(r0 + per_thread, a.n_requests);
   int32_t mine = 0;
   for (int r = r0; r < r1; ++r)
-    mine += kv_cost(kv_units(a, kv_span<ST>(a, a.lengths[r]))) * heads;
+    mine += kv_cost<S>(kv_units(a, kv_span<ST>(a, a.lengths[r]))) * heads;
   int32_t incl = mine;
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
@@ -401,7 +429,7 @@ __global__ __launch_bounds__(kKvBlock, OCC) void kv_attention_kernel(KvAttention
     total += scan[w];
   }
   total = uniform(total);
-  const KvShares shares = kv_shares(total, gridDim.x);
+  const KvShares shares = kv_shares(total, gridDim.x, S::LONG_RUN);
   if ((int32_t)blockIdx.x >= shares.runs) return;   // the whole workgroup
   const int32_t d0 = kv_begin(shares, blockIdx.x), d1 = kv_begin(shares, blockIdx.x + 1);
   if (before <= d0 && d0 < before + mine) {
@@ -409,7 +437,7 @@ __global__ __launch_bounds__(kKvBlock, OCC) void kv_attention_kernel(KvAttention
     int32_t length;
     for (;; ++r) {
       length = a.lengths[r];
-      const int32_t cost = kv_cost(kv_units(a, kv_span<ST>(a, length))) * heads;
+      const int32_t cost = kv_cost<S>(kv_units(a, kv_span<ST>(a, length))) * heads;
       if (d0 < before + cost) break;
       before += cost;
     }
@@ -433,7 +461,7 @@ __global__ __launch_bounds__(kKvBlock, OCC) void kv_attention_kernel(KvAttention
     const int r = uniform(row_r);
     const int32_t request_at = uniform(row_before);
     const KvSpan x = kv_span<ST>(a, uniform(row_length));
-    const int32_t units = kv_units(a, x), cost = kv_cost(units);
+    const int32_t units = kv_units(a, x), cost = kv_cost<S>(units);
     int hc0 = d0 > request_at ? (uint32_t)(d0 - request_at) / (uint32_t)cost : 0;
     for (; hc0 < heads; ++hc0) {
       const int hc = uniform(hc0);
@@ -551,7 +579,8 @@ __global__ __launch_bounds__(kKvBlock, OCC) void kv_attention_kernel(KvAttention
 #pragma unroll
           for (int i = 0; i < S::KL; ++i) {
             if (EXACT || i * (64 / (int)sizeof(C)) + g * (16 / (int)sizeof(C)) < D) {
-              const u32x4 v = ld_stream(reinterpret_cast<const u32x4*>(p + i * 64));
+              // kept in L1: the other half of a 128-byte line is the next load's
+              const u32x4 v = *reinterpret_cast<const u32x4*>(p + i * 64);
 #pragma unroll
               for (int e = 0; e < 4; ++e) kr[ts][i][e] = v[e];
             } else {
@@ -987,16 +1016,16 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
 
   // every wavefront adds the costs up by itself: at most 64 requests
   const int32_t cost = lane < a.n_requests
-                           ? kv_cost(kv_units(a, kv_span<S::ST>(a, a.lengths[lane]))) : 0;
+                           ? kv_cost<S>(kv_units(a, kv_span<S::ST>(a, a.lengths[lane]))) : 0;
   int32_t total = cost, before = lane < r ? cost : 0;
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
     total += __shfl_xor(total, d);
     before += __shfl_xor(before, d);
   }
-  const KvShares shares = kv_shares(uniform(total) * heads, most);
+  const KvShares shares = kv_shares(uniform(total) * heads, most, S::LONG_RUN);
   const int32_t units = kv_units(a, kv_span<S::ST>(a, scalar_load(a.lengths, r)));
-  const int32_t row_cost = kv_cost(units);
+  const int32_t row_cost = kv_cost<S>(units);
   const KvJoin j = kv_join_of(
       shares, KvCut{r, hc, uniform(before) * heads + (hc + 1) * row_cost - units, units});
   if (units == 0 || j.b0 == j.b1) return;        // written by its only part
@@ -1034,18 +1063,19 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttentionArgs 
 
 template <typename C, typename Q, int DPAD, int NB>
 hipError_t launch_kv_attention_shape(KvAttentionArgs a, hipStream_t s) {
-  // Workgroups per CU, all resident at once (what registers and LDS leave):
-  // the runs are equal, so a grid of more would only be cut finer. Twice as
-  // many workgroups took 3% longer on 2.3 GB and 10% on 190 MB; three waves a
-  // SIMD, where the registers of a type allow them, were no faster.
+  // Workgroups per CU at most, all resident at once (what registers and LDS
+  // leave): the runs are equal, so a grid of more would only be cut finer.
+  // Twice as many took 10% longer on 190 MB of mixed rows; three waves a SIMD,
+  // where the registers of a type allow them, 2 to 5% longer.
   constexpr int OCC = DPAD == 256 ? 1 : 2;
   const int chunks = (a.group + 16 * NB - 1) / (16 * NB);
   // no more workgroups than units at the table's full width
-  const int64_t steps = a.table_tokens / KvShape<C, Q, DPAD, NB>::ST + 3;
+  typedef KvShape<C, Q, DPAD, NB> S;
+  const int64_t steps = a.table_tokens / S::ST + 3;
   const int64_t rows = (int64_t)a.n_requests * a.n_kv_heads * chunks;
   a.step_shift = 0;
-  while (rows * ((steps >> a.step_shift) + 1 + kKvRowCost) > (int64_t(1) << 30)) ++a.step_shift;
-  const int64_t units = rows * ((steps >> a.step_shift) + 1 + kKvRowCost);
+  while (rows * ((steps >> a.step_shift) + 1 + S::ROW_COST) > (int64_t(1) << 30)) ++a.step_shift;
+  const int64_t units = rows * ((steps >> a.step_shift) + 1 + S::ROW_COST);
   const int64_t most = kKvCus * OCC;
   const unsigned blocks = (unsigned)std::min(std::max<int64_t>(units / kKvMinRun, 1), most);
   // Rows that can be cut into more than kKvFlatJoin parts each are joined by a
