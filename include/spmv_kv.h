@@ -172,6 +172,8 @@ SPMV_API spmv_status_t spmv_kv_append(const spmv_kv_cache_t* cache, int64_t n_to
  * aligned, zero-filled before its first use and left to this call alone from
  * then on (each call leaves what the next one needs); calls that may overlap
  * need one each. The size does not depend on n_requests or lengths.
+ * One launch, or two where few rows can be cut into many parts (at most 64
+ * requests, 32 rows of them and a table wide enough).
  * SPMV_ERR_INVALID_ARG for a bad cache, size, type, overlap, a negative
  * window or sinks, a scale that is not finite or a short workspace;
  * SPMV_ERR_UNSUPPORTED when table_width * page_size passes 2^31 - 65 or

@@ -1,7 +1,10 @@
 // New keys and values to their slots (spmv_kv_append): a scatter of whole
 // rows of head_dim elements, bound by copy bandwidth (each element is read
 // and written once) and, for the few tokens of a decoding step, by latency.
-// One thread per 16 bytes of k and of v; keys and values in one launch.
+// One thread per 16 bytes of k and of v, so that a wavefront's loads and stores
+// are whole lines of one or a few rows; keys and values in one launch. 16387
+// f16 tokens of 8 heads of 128 (134 MB read and written) take 29 us, 4.6 TB/s,
+// where a copy of 2 GiB reaches 4.85; 64 tokens 2.8 us.
 #include <hip/hip_runtime.h>
 
 #include "device_common.hpp"

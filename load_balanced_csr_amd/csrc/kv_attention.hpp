@@ -44,8 +44,8 @@
 // addresses 2.5, the first loads 2, and at the end LDS, the parts' stores, the
 // counter and the join 3.5.
 // Looked at and not kept: loads of the next row begun under the last step of
-// the one before (3% slower: its coordinates do not fit the scalar registers
-// beside the row's), one key head for each wavefront (2% faster on large rows
+// the one before (1% slower on large rows, 23% on short f32 ones: two rows'
+// coordinates do not fit the scalar registers), one key head for each wavefront (2% faster on large rows
 // of many heads, 4% slower on mixed ones, 15% on one short row), 64-token
 // steps for rows of 128 bytes (5% slower on 96 rows of 8-bit keys).
 #pragma once

@@ -87,6 +87,21 @@ def _ints(t, name: str, n: int) -> int:
     raise ValueError("%s has %d entries, %d are needed" % (name, t.numel(), n))
 
 
+def _all_ints(names, tensors, sizes):
+    """Pointers of contiguous device int32 tensors of at least these sizes: the checks of
+    _ints in one loop, as a call that takes ten of them spends more on them than on its
+    launch otherwise."""
+    try:
+        for t, n in zip(tensors, sizes):
+            if not (t.dtype is _I32 and t.is_cuda and t.is_contiguous() and t.numel() >= n):
+                break
+        else:
+            return [t.data_ptr() for t in tensors]
+    except AttributeError:
+        pass
+    return [_ints(t, name, n) for name, t, n in zip(names, tensors, sizes)]
+
+
 def _table(t, n_requests: int):
     """Pointer, row stride and width of a block table of n_requests rows."""
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
@@ -133,6 +148,11 @@ def _outer(t, name: str) -> int:
     return t.shape[0]
 
 
+_GROW_NAMES = ("lengths", "n_new", "free_pages", "cursor", "lengths_out", "cursor_out",
+               "token_ptr", "slots", "status", "positions")
+_SHRINK_NAMES = ("lengths", "keep", "free_pages", "cursor", "lengths_out", "cursor_out", "status")
+
+
 def spmv_kv_grow(lengths, n_new, page_size: int, free_pages, cursor, table, lengths_out,
                  cursor_out, token_ptr, slots, positions, status, stream=None) -> None:
     """Pages for n_new[r] tokens more of each request, taken from free_pages from cursor on
@@ -144,13 +164,13 @@ def spmv_kv_grow(lengths, n_new, page_size: int, free_pages, cursor, table, leng
     n = lengths.numel()
     n_tokens = slots.numel()
     tp, ts, tw = _table(table, n)
-    _check(_load().spmv_kv_grow(
-        n, _ints(lengths, "lengths", n), _ints(n_new, "n_new", n), page_size,
-        _ints(free_pages, "free_pages", 0), free_pages.numel(), _ints(cursor, "cursor", 1),
-        tp, ts, tw, _ints(lengths_out, "lengths_out", n), _ints(cursor_out, "cursor_out", 1),
-        _ints(token_ptr, "token_ptr", n + 1), _ints(slots, "slots", 0),
-        None if positions is None else _ints(positions, "positions", n_tokens), n_tokens,
-        _ints(status, "status", 2), _stream(stream, status)), "spmv_kv_grow")
+    ln, nn, fp, cu, lo, co, pt, sl, st, po = _all_ints(
+        _GROW_NAMES, (lengths, n_new, free_pages, cursor, lengths_out, cursor_out, token_ptr,
+                      slots, status, slots if positions is None else positions),
+        (n, n, 0, 1, n, 1, n + 1, 0, 2, n_tokens))
+    _check(_load().spmv_kv_grow(n, ln, nn, page_size, fp, free_pages.numel(), cu, tp, ts, tw, lo,
+                                co, pt, sl, None if positions is None else po, n_tokens, st,
+                                _stream(stream, status)), "spmv_kv_grow")
 
 
 def spmv_kv_shrink(lengths, keep, page_size: int, free_pages, cursor, table, lengths_out,
@@ -160,11 +180,11 @@ def spmv_kv_shrink(lengths, keep, page_size: int, free_pages, cursor, table, len
     spmv_kv_grow."""
     n = lengths.numel()
     tp, ts, tw = _table(table, n)
-    _check(_load().spmv_kv_shrink(
-        n, _ints(lengths, "lengths", n), _ints(keep, "keep", n), page_size,
-        _ints(free_pages, "free_pages", 0), free_pages.numel(), _ints(cursor, "cursor", 1),
-        tp, ts, tw, _ints(lengths_out, "lengths_out", n), _ints(cursor_out, "cursor_out", 1),
-        _ints(status, "status", 2), _stream(stream, status)), "spmv_kv_shrink")
+    ln, ke, fp, cu, lo, co, st = _all_ints(
+        _SHRINK_NAMES, (lengths, keep, free_pages, cursor, lengths_out, cursor_out, status),
+        (n, n, 0, 1, n, 1, 2))
+    _check(_load().spmv_kv_shrink(n, ln, ke, page_size, fp, free_pages.numel(), cu, tp, ts, tw, lo,
+                                  co, st, _stream(stream, status)), "spmv_kv_shrink")
 
 
 class KvCache:
@@ -238,7 +258,9 @@ class KvCache:
         [n_requests, n_q_heads, head_dim], table the block table, lengths int32 with the
         newest token counted. window 0 sees every token, otherwise the last ``window`` and
         the first ``sinks``. scale: head_dim ** -0.5 unless given. lse: float32
-        [n_requests, n_q_heads] to receive the log of the softmax's sum. Returns out."""
+        [n_requests, n_q_heads] to receive the log of the softmax's sum. Returns out.
+
+        The first call on a stream allocates its workspace: make one before a capture."""
         n = _outer(q, "q")
         shape = q.shape
         heads = shape[1]
