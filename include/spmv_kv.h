@@ -155,6 +155,9 @@ SPMV_API spmv_status_t spmv_kv_append(const spmv_kv_cache_t* cache, int64_t n_to
  *   out[r][h][:] = sum_t exp(s[t] - m) v[t][:] / sum_t exp(s[t] - m), m = max s
  *   lse[r][h] = m + log(sum_t exp(s[t] - m))
  *
+ * Several new tokens of one request are several rows: the same table row, a
+ * length one higher each.
+ *
  * A row with no visible token (length 0), or none whose score is above -inf,
  * gives out = 0 and lse = -inf. A
  * length below 0 counts as 0, one beyond table_width * page_size as that; a

@@ -64,9 +64,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream, t):
-    """hipStream_t of `stream`, or of the current stream of t's device."""
+    """hipStream_t of `stream`, or of the current device's current stream; t, one of the
+    call's tensors, has to be on that device."""
+    device = torch.cuda.current_device()
+    if t.get_device() != device:
+        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d"
+                         % (t.get_device(), device))
     if stream is None and _raw_stream is not None:
-        return _raw_stream(t.get_device())
+        return _raw_stream(device)
     return _given_stream(stream)
 
 

@@ -144,6 +144,16 @@ def test_long_rows_are_split_and_joined(dtype, n):
     Case([n, 3, n // 3], Hq=4, H=1, D=128, P=64, dtype=dtype).check()
 
 
+@pytest.mark.parametrize("dtype,D,G", [(BF16, 256, 24), (F8, 256, 17), (F16, 128, 32), (F32, 256, 5),
+                                       (BF16, 192, 40), (F8, 128, 3), (F32, 80, 20)])
+def test_wide_heads_and_groups_joined_either_way(dtype, D, G):
+    """Few rows (their parts joined by a second launch), then more than 64 with a long one
+    among them (joined by the workgroups, in two levels), in whole pages and odd ones."""
+    for P in (64, 20):
+        Case([6000, 3, 40], Hq=G, H=1, D=D, P=P, dtype=dtype, seed=G).check()
+        Case([9000] + [5] * 70 + [0], Hq=G, H=1, D=D, P=P, dtype=dtype, seed=G + 1).check()
+
+
 def test_long_rows_beside_many_short_ones():
     Case([1 + 13 * (r % 9) for r in range(150)] + [9000] + [0, 1] * 20, Hq=8, H=2, D=64,
          seed=7).check()
