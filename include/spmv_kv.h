@@ -145,6 +145,8 @@ SPMV_API spmv_status_t spmv_kv_append(const spmv_kv_cache_t* cache, int64_t n_to
                                       int64_t v_token_stride, int64_t v_head_stride,
                                       int32_t dtype, const int32_t* slots, hipStream_t stream);
 
+#define SPMV_KV_WORKSPACE_ZEROED 8192
+
 /* Attention of one new token per request over its cached tokens. Request r
  * (the row) has lengths[r] tokens, the newest among them; token t is visible
  * when t >= lengths[r] - window or t < sinks (window 0: every token; the
@@ -172,9 +174,9 @@ SPMV_API spmv_status_t spmv_kv_append(const spmv_kv_cache_t* cache, int64_t n_to
  * table   block table (see above), lengths int32[n_requests].
  * Scores, maxima, sums and the output's sums are held in 32 bits.
  * workspace: at least spmv_kv_attention_workspace_size(..) bytes, 16-byte
- * aligned, zero-filled before its first use and left to this call alone from
- * then on (each call leaves what the next one needs); calls that may overlap
- * need one each. The size does not depend on n_requests or lengths.
+ * aligned, its first SPMV_KV_WORKSPACE_ZEROED bytes 0 before its first use and
+ * left to this call alone from then on (each call leaves what the next one
+ * needs); calls that may overlap need one each. The size does not depend on n_requests or lengths.
  * One launch, or two where few rows can be cut into many parts (at most 64
  * requests, 32 rows of them and a table wide enough).
  * SPMV_ERR_INVALID_ARG for a bad cache, size, type, overlap, a negative

@@ -83,6 +83,7 @@ constexpr int kv_row_blocks(int group, int cache_dtype) {
 constexpr size_t kv_slot_floats(int nb, int dpad) { return (size_t)16 * nb * (dpad + 2); }
 // two counters for each slot: arrivals at a group of parts, and of groups at a row
 constexpr size_t kKvCounterBytes = 4 * kKvMaxBlocks * sizeof(int32_t);
+static_assert(kKvCounterBytes == SPMV_KV_WORKSPACE_ZEROED, "the counters come first");
 constexpr int kKvFlatJoin = 16;
 // Units (steps and row costs) of the shortest run one workgroup takes.
 constexpr int kKvMinRun = 4;
@@ -1069,9 +1070,12 @@ hipError_t launch_kv_attention_shape(KvAttentionArgs a, hipStream_t s) {
   // where the registers of a type allow them, 2 to 5% longer.
   constexpr int OCC = DPAD == 256 ? 1 : 2;
   const int chunks = (a.group + 16 * NB - 1) / (16 * NB);
-  // no more workgroups than units at the table's full width
+  // no more workgroups than units with every row at the table's full width (or the window's
+  // and the first tokens', each of which can begin or end inside a step)
   typedef KvShape<C, Q, DPAD, NB> S;
-  const int64_t steps = a.table_tokens / S::ST + 3;
+  int64_t tokens = a.table_tokens;
+  if (a.window) tokens = std::min<int64_t>(tokens, (int64_t)a.window + a.sinks);
+  const int64_t steps = tokens / S::ST + 4;
   const int64_t rows = (int64_t)a.n_requests * a.n_kv_heads * chunks;
   a.step_shift = 0;
   while (rows * ((steps >> a.step_shift) + 1 + S::ROW_COST) > (int64_t(1) << 30)) ++a.step_shift;

@@ -20,6 +20,7 @@ from .binding import _check, _stream as _given_stream
 KV_F32, KV_F16, KV_BF16, KV_F8E4M3 = 0, 1, 2, 3
 KV_DTYPE = {torch.float32: KV_F32, torch.float16: KV_F16, torch.bfloat16: KV_BF16,
             torch.float8_e4m3fn: KV_F8E4M3}
+KV_WORKSPACE_ZEROED = 8192       # bytes at a workspace's start that begin as 0
 KV_OK, KV_NO_PAGES, KV_BAD_ROW, KV_NO_ROOM = 0, 1, 2, 3
 
 KV_EXPORTED = ("spmv_kv_grow", "spmv_kv_shrink", "spmv_kv_append",
@@ -247,7 +248,8 @@ class KvCache:
                "spmv_kv_append")
 
     def workspace_size(self, n_q_heads: int) -> int:
-        """Bytes of workspace attend() needs; the tensor given must be zero-filled once."""
+        """Bytes of workspace attend() needs; the first KV_WORKSPACE_ZEROED of the tensor
+        given must be 0 before its first use."""
         need = self._need.get(n_q_heads)
         if need is None:
             b = ctypes.c_size_t(0)
@@ -293,7 +295,8 @@ class KvCache:
             workspace = self._ws.get(handle)
             if workspace is None or workspace.numel() < need:
                 with _on(stream):
-                    workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
+                    workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+                    workspace[:KV_WORKSPACE_ZEROED].zero_()
                 self._ws[handle] = workspace
         elif not workspace.is_cuda or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous device tensor")

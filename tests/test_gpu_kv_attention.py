@@ -298,7 +298,8 @@ def test_a_workspace_serves_calls_of_other_shapes():
     cases = [Case([6000, 100], Hq=8, H=2, D=128), Case([3] * 40, Hq=8, H=2, D=128, seed=1),
              Case([1, 0, 9000], Hq=8, H=2, D=128, seed=2)]
     need = max(c.cache().workspace_size(8) for c in cases)
-    ws = torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda")
+    ws = torch.full((max(need, 16),), 0xa5, dtype=torch.uint8, device="cuda")
+    ws[:lb.kv.KV_WORKSPACE_ZEROED] = 0
     wants = [c.ref() for c in cases]
     for turn in range(3):
         for c, w in zip(cases, wants):

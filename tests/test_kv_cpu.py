@@ -23,6 +23,8 @@ def test_header_and_binding_agree():
     assert names == set(lb.KV_EXPORTED)
     for name in names:
         assert hasattr(lb.load(), name), name
+    assert int(re.search(r"define SPMV_KV_WORKSPACE_ZEROED (\d+)", src).group(1)) == \
+        kv.KV_WORKSPACE_ZEROED
 
 
 def test_struct_layout_matches_the_header(tmp_path):
