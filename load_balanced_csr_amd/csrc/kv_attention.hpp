@@ -172,6 +172,13 @@ __device__ __forceinline__ void share4(float* p, f32x4 x) {
                                   (uint64_t)__float_as_uint(x[2 * h + 1]) << 32,
                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+// This wavefront's share() stores have arrived; followed by a barrier, all of
+// the workgroup's. (The fence inside a barrier orders a workgroup, whose
+// wavefronts share an L1; it does not wait for stores to reach memory.)
+__device__ __forceinline__ void shares_done() {
+  memory_order_point();
+  wait_vmem();
+}
 __device__ __forceinline__ float shared(const float* p) {
   return __hip_atomic_load(const_cast<float*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -928,7 +935,7 @@ __global__ __launch_bounds__(kKvBlock, OCC) void kv_attention_kernel(KvAttention
   // (told only here, when the stores of both have long been under way)
   int32_t* counters = static_cast<int32_t*>(a.workspace);
   KvJoin h = kv_join_of(shares, head_cut), t = kv_join_of(shares, tail_cut);
-  wait_vmem();                                   // this wavefront's stores are done
+  shares_done();
   __syncthreads();
   const int32_t b = blockIdx.x;
   if (tid == 0) {
@@ -982,7 +989,7 @@ __global__ __launch_bounds__(kKvBlock, OCC) void kv_attention_kernel(KvAttention
         share(first + ROWS + row, wave_l[end][row]);
       }
     }
-    wait_vmem();
+    shares_done();
     __syncthreads();
     if (tid == 0) {
       int32_t* rows_counters = counters + 2 * kKvMaxBlocks;
