@@ -293,6 +293,23 @@ def test_results_are_the_same_bits_every_time_and_on_another_stream():
         assert torch.equal(out, first), i
 
 
+def test_calls_on_two_streams_at_once():
+    """One cache, calls that split rows on two streams with nothing between them: each
+    stream has a workspace of its own."""
+    c = Case([7000, 300, 5], Hq=8, H=2, D=128, seed=6)
+    cache = c.cache()
+    q, table, lengths = c.q.cuda(), c.table.cuda(), c.lengths.cuda()
+    want = cache.attend(q, table, lengths)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.empty_like(q) for _ in range(20)] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for s, out in zip(streams, outs):
+            cache.attend(q, table, lengths, out[i], stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for out in outs for o in out)
+
+
 def test_a_workspace_serves_calls_of_other_shapes():
     """One workspace, calls that split long rows and calls that do not, in turn."""
     cases = [Case([6000, 100], Hq=8, H=2, D=128), Case([3] * 40, Hq=8, H=2, D=128, seed=1),
